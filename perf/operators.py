@@ -241,7 +241,8 @@ def prepare(case, seed):
     s["lse"] = torch.empty(rows, heads, device=device)
     if own:
         import paged_mqa_logits_indexer_amd as lib
-        n = lib.attention_workspace_bytes(rows, heads, requests)
+        size = lib.shared_prefix_workspace_bytes if case["op"] == "shared" else lib.attention_workspace_bytes
+        n = size(rows, heads, requests)
         s["workspace"] = torch.empty(n, dtype=torch.uint8, device=device)
     return s
 
