@@ -63,6 +63,10 @@ typedef enum {
  * to the same FP16 value tie ([P3] Summary). */
 typedef enum { IDX_KEY_FP32 = 0, IDX_KEY_FP16 = 1 } idx_key_dtype;
 
+/* Element type of rows and caches of the appends and of the attention.  FP32
+ * is taken by the index-key appends only. */
+typedef enum { IDX_BF16 = 0, IDX_FP16 = 1, IDX_FP32 = 2 } idx_value_dtype;
+
 /* Fixed shape of the method ([P1] "What this adds": H = 32, D = 128). */
 #define IDX_NUM_HEADS 32
 #define IDX_HEAD_DIM 128
@@ -74,6 +78,14 @@ typedef enum { IDX_KEY_FP32 = 0, IDX_KEY_FP16 = 1 } idx_key_dtype;
 /* topk_rows: rows of more than 16384 scores go through the chunked path,
  * whose strides are limited to 2^23 (8x the longest context on the pages). */
 #define IDX_TOPK_MAX_STRIDE (1 << 23)
+/* Latent cache row: 512 latent dimensions (which are also the value vector)
+ * and 64 rotated ones.  The first 64 dimensions of an index key are rotated. */
+#define IDX_LATENT_DIM 512
+#define IDX_ROPE_DIM 64
+#define IDX_LATENT_ROW 576
+#define IDX_MAX_ATTENTION_HEADS 128
+#define IDX_MAX_APPEND_TOKENS (1 << 24)
+#define IDX_MAX_CACHE_PAGES ((1 << 25) - 1) /* 64 * pages stays a 32-bit integer */
 /* topk_rows_noalloc: rows its fixed scratch holds (chunked path only). */
 #define IDX_NOALLOC_MAX_ROWS 128
 
@@ -427,6 +439,152 @@ idx_status topk_rows_f16(const uint16_t* logits, int64_t logits_stride,
                          const int32_t* hist, const int32_t* context_lens,
                          int32_t rows, int32_t k, int32_t* indices,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Appending to the paged caches.  Row t of the input is rotated by position
+ * positions[t] and written to cache slot slots[t] = page * 64 + place; a slot
+ * that is negative or not in the cache writes nothing (padding of a batch).
+ * Slots of one call are distinct (a slot given twice holds a mix of its rows).
+ *
+ * Rotation: of 64 dimensions, pair (a, b) with index i < 32 becomes
+ * (a c_i - b s_i, b c_i + a s_i), where rope[p] = c_0 .. c_31, s_0 .. s_31.
+ * The pairs are dimensions (i, i + 32), or (2i, 2i + 1) with interleaved != 0.
+ * It is computed beyond float32 and rounded once.
+ *
+ * positions    (device) int32 [tokens], clamped to [0, max_positions)
+ * slots        (device) int32 [tokens]
+ * rope         (device) float [max_positions][64], 16-B aligned
+ * tokens       1 .. IDX_MAX_APPEND_TOKENS; num_pages 1 .. IDX_MAX_CACHE_PAGES
+ * row strides  in elements; rows are 16-B aligned (pointer and stride) and do
+ *              not overlap the cache
+ * Errors: IDX_EINVAL (NULL pointer, non-positive size, stride below the row),
+ * IDX_EUNSUPPORTED (type, limits), IDX_EALIGN, IDX_ELAUNCH.
+ *
+ * index_k_append -- index keys as FP8 E4M3FN codes with one scale per token,
+ * the layout indexer_logits reads: y = the key with dimensions 0..63 rotated,
+ * scale = max|y| / 448 (float32; 0 for a key of zeros), code = e4m3(y / scale)
+ * to nearest even.  A key with a NaN or an infinity gets codes 0 and the
+ * scale NaN: its logits are NaN, which topk_rows never selects.
+ *
+ * k            (device) [tokens] rows of 128, k_dtype BF16, FP16 or FP32
+ * kv_pages     (device) uint8 [num_pages][64][128], 16-B aligned
+ * k_scales     (device) float [num_pages][64]
+ */
+idx_status index_k_append(const void* k, int64_t k_stride, int32_t k_dtype, const int32_t* positions,
+                          const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                          int32_t tokens, int32_t num_pages, uint8_t* kv_pages, float* k_scales, void* stream);
+
+/*
+ * index_k_append_mxfp4 -- index_k_append into packed MXFP4 tokens, the layout
+ * indexer_logits_mxfp4 reads: per block of 32 dimensions the power of two
+ * 2^(floor(log2 max|y|) - 2) as an E8M0 byte (at least 2^-127) and E2M1 codes
+ * of y over it, to nearest even, magnitudes above 6 to 6.  A block with a NaN
+ * or an infinity gets codes 0 and the byte 255 (NaN).
+ *
+ * kv_pages     (device) uint8 [num_pages][64][68], 16-B aligned
+ */
+idx_status index_k_append_mxfp4(const void* k, int64_t k_stride, int32_t k_dtype, const int32_t* positions,
+                                const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                                int32_t tokens, int32_t num_pages, uint8_t* kv_pages, void* stream);
+
+/*
+ * latent_append -- rows of 512 latent and 64 rotated dimensions into the
+ * latent cache: the latent part bit by bit, the rotated part (dimensions
+ * 512..575) rounded to nearest even.
+ *
+ * kv           (device) [tokens] rows of 576, dtype BF16 or FP16
+ * latent_pages (device) [num_pages][64][576] of the same type, 16-B aligned
+ */
+idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const int32_t* positions,
+                         const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                         int32_t tokens, int32_t num_pages, void* latent_pages, void* stream);
+
+/*
+ * Attention over the latent cache.  All heads of a row read the same cache
+ * row per key: with k_s the 576 values of key s and v_s its first 512,
+ *
+ *   z = scale * q . k_s;   z = softcap * tanh(z / softcap)  if softcap > 0;
+ *   z = z - slopes[h] * |position_r - s|                    if slopes
+ *   out[r][h] = sum_s softmax_s(z) v_s,    lse[r][h] = log sum_s exp(z)
+ *
+ * over the keys s that row r sees; a row that sees none gets out = 0 and
+ * lse = -infinity.  Key s of a request is slot s % 64 of page
+ * block_table[request][s / 64].  Products and the softmax are summed in
+ * float32; the softmax weights are rounded to the cache's type for the product
+ * with the values.  What the cache holds at keys a row does not see, NaN and
+ * infinities included, does not reach that row.  A row that sees a NaN, or
+ * whose score is +infinity, is NaN.
+ *
+ * q            (device) [rows][heads][576], dtype BF16 or FP16, 16-B aligned
+ * latent_pages (device) [num_pages][64][576] of the same type, 16-B aligned
+ * block_table  (device) int32 [requests][max_pages]; ids clamped into the cache
+ * requests     1 .. IDX_MAX_REQUESTS; rows 1 .. IDX_MAX_ROWS;
+ *              heads 1 .. IDX_MAX_ATTENTION_HEADS;
+ *              num_pages, max_pages 1 .. IDX_MAX_CACHE_PAGES, requests * max_pages < 2^31
+ * next_n, cu_q next_n > 0 and cu_q NULL: rows = requests * next_n, row r
+ *              belongs to request r / next_n.  next_n 0 and cu_q (device)
+ *              int32 [requests + 1], ascending: request b owns rows cu_q[b] ..
+ *              cu_q[b+1]-1; rows of no request are not written.
+ * scale        finite; softcap finite, >= 0
+ * slopes       (device) float [heads], or NULL: no distance bias
+ * row_positions(device) int32 [rows], or NULL: row_lens - 1
+ * out          (device) [rows][heads][512] of q's type, 16-B aligned
+ * lse          (device) float [rows][heads], or NULL
+ * workspace    (device) scratch of at least attention_workspace_bytes(rows,
+ *              heads, requests) bytes, 256-B aligned; needs no initialisation.
+ *              Calls that share a workspace must be ordered on one stream.
+ * Errors: IDX_EINVAL (NULL pointer, non-positive size, next_n and cu_q both or
+ * neither, rows != requests * next_n, scale or softcap), IDX_EUNSUPPORTED
+ * (type, limits), IDX_EALIGN, IDX_EWORKSPACE, IDX_ELAUNCH.
+ *
+ * paged_attention -- row r sees keys row_starts[r] <= s < row_lens[r]: causal
+ * rows have row_lens = position + 1; a sliding window or a document mask moves
+ * row_starts, a prefix mask raises row_lens.
+ *
+ * row_lens     (device) int32 [rows], clamped to [0, 64 max_pages]
+ * row_starts   (device) int32 [rows], or NULL: 0
+ */
+size_t attention_workspace_bytes(int32_t rows, int32_t heads, int32_t requests);
+
+idx_status paged_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                           const int32_t* row_lens, const int32_t* row_starts, const int32_t* cu_q, int32_t rows,
+                           int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages,
+                           float scale, float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * shared_prefix_attention -- paged_attention for a batch whose requests share
+ * their first prefix_pages pages: the first prefix_pages entries of every
+ * block-table row are the same (those of row 0 are used).  The shared keys are
+ * read once for the rows of all requests.  Arguments and results as for
+ * paged_attention with next_n rows per request; the workspace holds
+ * shared_prefix_workspace_bytes(rows, heads, requests).
+ *
+ * prefix_pages 1 .. max_pages
+ */
+size_t shared_prefix_workspace_bytes(int32_t rows, int32_t heads, int32_t requests);
+
+idx_status shared_prefix_attention(const void* q, const void* latent_pages, int32_t dtype,
+                                   const int32_t* block_table, const int32_t* row_lens, const int32_t* row_starts,
+                                   int32_t rows, int32_t heads, int32_t requests, int32_t next_n,
+                                   int32_t prefix_pages, int32_t num_pages, int32_t max_pages, float scale,
+                                   float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sparse_attention -- attention of every row over the keys that the top-k
+ * selected for it: indices[r] lists logical key positions of row r's request
+ * as topk_rows and sparse_topk give them, in any order; entries outside
+ * [0, 64 max_pages) (the -1 padding) are skipped wherever they stand, and a
+ * key listed twice counts twice.  Slopes need row_positions here.
+ *
+ * indices      (device) int32 [rows][k], k in 1 .. IDX_CANDIDATE_CAPACITY
+ */
+idx_status sparse_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                            const int32_t* indices, int32_t k, const int32_t* cu_q, int32_t rows, int32_t heads,
+                            int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages, float scale,
+                            float softcap, const float* slopes, const int32_t* row_positions, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * indexer_time_next_call -- measurement aid.  Arms the calling host thread:

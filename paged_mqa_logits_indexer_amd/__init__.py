@@ -28,6 +28,13 @@ Entry points (same names as the C ABI):
                         context_lens, logits)
   sparse_to_logical(indices, table, out)
   sparse_topk(scores, hist, sparse_lens, k, key_dtype, table, out)
+  index_k_append(k, positions, slots, rope, kv_pages, k_scales, interleaved)  paged caches:
+  index_k_append_mxfp4(k, positions, slots, rope, kv_pages, interleaved)
+  latent_append(kv, positions, slots, rope, latent_pages, interleaved)
+  paged_attention(q, latent_pages, block_table, row_lens, next_n, scale, out, ...)
+  shared_prefix_attention(..., next_n, prefix_pages, scale, out, ...)
+  sparse_attention(q, latent_pages, block_table, indices, next_n, scale, out, ...)
+  attention_workspace_bytes(rows, heads, requests), shared_prefix_workspace_bytes(...)
   indexer_status_str(status)
   indexer_time_next_call(start, stop)
   hbm_read_probe(src, sink, events=None)
@@ -66,6 +73,10 @@ HEADS = 32
 HEAD_DIM = 128
 PAGE_TOKENS = 64
 MXFP4_TOKEN_BYTES = 68
+LATENT_DIM = 512
+ROPE_DIM = 64
+LATENT_ROW = 576
+VALUE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 EXPORTED_SYMBOLS = ("indexer_logits", "indexer_logits_f16", "indexer_logits_mxfp4", "block_amax8",
                     "sort_candidate_blocks", "indexer_sparse_logits", "indexer_sparse_logits_mxfp4",
@@ -73,7 +84,9 @@ EXPORTED_SYMBOLS = ("indexer_logits", "indexer_logits_f16", "indexer_logits_mxfp
                     "topk_workspace_bytes", "topk_rows", "topk_rows_noalloc",
                     "topk_rows_f16", "score_histogram", "indexer_status_str",
                     "indexer_time_next_call", "hbm_read_probe", "hbm_read_probe_nt", "hbm_gather_probe",
-                    "mfma_valu_probe")
+                    "mfma_valu_probe", "index_k_append", "index_k_append_mxfp4", "latent_append",
+                    "attention_workspace_bytes", "shared_prefix_workspace_bytes", "paged_attention",
+                    "shared_prefix_attention", "sparse_attention")
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libpaged_mqa_indexer.so"
@@ -148,6 +161,25 @@ def load_library() -> ctypes.CDLL:
     lib.topk_rows_noalloc.restype = ctypes.c_int
     lib.indexer_time_next_call.argtypes = [vp, vp]
     lib.indexer_time_next_call.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.index_k_append.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+    lib.index_k_append.restype = ctypes.c_int
+    lib.index_k_append_mxfp4.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.index_k_append_mxfp4.restype = ctypes.c_int
+    lib.latent_append.argtypes = lib.index_k_append_mxfp4.argtypes
+    lib.latent_append.restype = ctypes.c_int
+    for name in ("attention_workspace_bytes", "shared_prefix_workspace_bytes"):
+        getattr(lib, name).argtypes = [i32, i32, i32]
+        getattr(lib, name).restype = sz
+    lib.paged_attention.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, vp,
+                                    vp, vp, vp, sz, vp]
+    lib.paged_attention.restype = ctypes.c_int
+    lib.shared_prefix_attention.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, f32,
+                                            vp, vp, vp, vp, vp, sz, vp]
+    lib.shared_prefix_attention.restype = ctypes.c_int
+    lib.sparse_attention.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, vp,
+                                     vp, vp, vp, sz, vp]
+    lib.sparse_attention.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -556,6 +588,183 @@ def score_histogram(scores, context_lens, hist):
         st = lib.score_histogram(_ptr(scores), int(scores.stride(0)), _ptr(context_lens),
                                  int(rows), _ptr(hist), _stream_ptr(dev))
     _check("score_histogram", st)
+
+
+def _append_call(name, dim, dtypes, rows, positions, slots, rope, pages, tail, interleaved, events):
+    dev = rows.device
+    if rows.dtype not in dtypes:
+        raise TypeError(f"rows must be one of {dtypes}, got {rows.dtype}")
+    _need(rows, "rows", rows.dtype, dev, 2)
+    _need(positions, "positions", torch.int32, dev, 1)
+    _need(slots, "slots", torch.int32, dev, 1)
+    _need(rope, "rope", torch.float32, dev, 2)
+    tokens = rows.shape[0]
+    if rows.shape[1] != dim or rows.stride(1) != 1:
+        raise ValueError(f"rows must be [tokens, {dim}] with unit column stride")
+    if positions.shape[0] != tokens or slots.shape[0] != tokens or not (
+            positions.is_contiguous() and slots.is_contiguous()):
+        raise ValueError(f"positions and slots must be contiguous [{tokens}]")
+    if rope.shape[1] != ROPE_DIM or not rope.is_contiguous():
+        raise ValueError("rope must be contiguous [max_positions, 64]")
+    # the stride of a single row carries no meaning
+    stride = rows.stride(0) if tokens > 1 else dim
+    lib = load_library()
+    with torch.cuda.device(dev):
+        _arm(events, dev)
+        st = getattr(lib, name)(_ptr(rows), stride, VALUE_DTYPES[rows.dtype], _ptr(positions), _ptr(slots),
+                                _ptr(rope), rope.shape[0], int(bool(interleaved)), tokens, pages.shape[0],
+                                _ptr(pages), *tail, _stream_ptr(dev))
+    _check(name, st)
+
+
+def _need_pages(t, name, dtype, dev, width):
+    _need(t, name, dtype, dev, 3)
+    if t.shape[1] != PAGE_TOKENS or t.shape[2] != width or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [P, 64, {width}]")
+
+
+def index_k_append(k, positions, slots, rope, kv_pages, k_scales, interleaved=False, events=None):
+    """Rotate index keys by their positions and append them to the FP8 cache.
+
+    k [tokens, 128] bfloat16, float16 or float32 with unit column stride and
+    16-byte rows (a slice of a wider tensor is fine); positions [tokens] int32;
+    slots [tokens] int32 = page * 64 + place, negative to write nothing; rope
+    [max_positions, 64] float32, 32 cosines then 32 sines; kv_pages [P, 64, 128]
+    uint8 and k_scales [P, 64] float32 as indexer_logits reads them.  The first
+    64 dimensions are rotated in pairs (i, i + 32), or (2i, 2i + 1) with
+    ``interleaved``.
+    """
+    _need_pages(kv_pages, "kv_pages", torch.uint8, k.device, HEAD_DIM)
+    _need(k_scales, "k_scales", torch.float32, k.device, 2)
+    if tuple(k_scales.shape) != (kv_pages.shape[0], PAGE_TOKENS) or not k_scales.is_contiguous():
+        raise ValueError("k_scales must be contiguous [P, 64]")
+    _append_call("index_k_append", HEAD_DIM, (torch.bfloat16, torch.float16, torch.float32), k, positions, slots,
+                 rope, kv_pages, (_ptr(k_scales),), interleaved, events)
+
+
+def index_k_append_mxfp4(k, positions, slots, rope, kv_pages, interleaved=False, events=None):
+    """index_k_append into packed MXFP4 tokens: kv_pages [P, 64, 68] uint8."""
+    _need_pages(kv_pages, "kv_pages", torch.uint8, k.device, MXFP4_TOKEN_BYTES)
+    _append_call("index_k_append_mxfp4", HEAD_DIM, (torch.bfloat16, torch.float16, torch.float32), k, positions,
+                 slots, rope, kv_pages, (), interleaved, events)
+
+
+def latent_append(kv, positions, slots, rope, latent_pages, interleaved=False, events=None):
+    """Append rows of 512 latent and 64 rotated dimensions to the latent cache.
+
+    kv [tokens, 576] bfloat16 or float16 (unit column stride, 16-byte rows);
+    latent_pages [P, 64, 576] of the same type; positions, slots, rope and
+    ``interleaved`` as for index_k_append; dimensions 512..575 are rotated.
+    """
+    _need_pages(latent_pages, "latent_pages", kv.dtype, kv.device, LATENT_ROW)
+    _append_call("latent_append", LATENT_ROW, (torch.bfloat16, torch.float16), kv, positions, slots, rope,
+                 latent_pages, (), interleaved, events)
+
+
+def attention_workspace_bytes(rows: int, heads: int, requests: int) -> int:
+    """Workspace of paged_attention and sparse_attention."""
+    return int(load_library().attention_workspace_bytes(int(rows), int(heads), int(requests)))
+
+
+def shared_prefix_workspace_bytes(rows: int, heads: int, requests: int) -> int:
+    return int(load_library().shared_prefix_workspace_bytes(int(rows), int(heads), int(requests)))
+
+
+def _attention_call(name, q, latent_pages, block_table, keys, next_n, cu_q, starts, prefix_pages, scale, out, lse,
+                    softcap, slopes, row_positions, workspace, events):
+    """keys: row_lens [rows], or the selected keys [rows, k] (sparse_attention)."""
+    dev = q.device
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    _need(q, "q", q.dtype, dev, 3)
+    rows, heads, dim = q.shape
+    if dim != LATENT_ROW or not q.is_contiguous():
+        raise ValueError("q must be contiguous [rows, heads, 576]")
+    _need_pages(latent_pages, "latent_pages", q.dtype, dev, LATENT_ROW)
+    _rows2(block_table, "block_table", torch.int32, dev)
+    requests, max_pages = block_table.shape
+    sparse = name == "sparse_attention"
+    _need(keys, "indices" if sparse else "row_lens", torch.int32, dev, 2 if sparse else 1)
+    if keys.shape[0] != rows or not keys.is_contiguous():
+        raise ValueError("indices must be contiguous [rows, k]" if sparse else "row_lens must be contiguous [rows]")
+    for t, what, dtype, n in ((starts, "row_starts", torch.int32, rows), (cu_q, "cu_q", torch.int32, requests + 1),
+                              (row_positions, "row_positions", torch.int32, rows),
+                              (slopes, "slopes", torch.float32, heads)):
+        if t is not None:
+            _need(t, what, dtype, dev, 1)
+            if t.shape[0] != n or not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous [{n}]")
+    _need(out, "out", q.dtype, dev, 3)
+    if tuple(out.shape) != (rows, heads, LATENT_DIM) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous [{rows}, {heads}, 512]")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev, 2)
+        if tuple(lse.shape) != (rows, heads) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{rows}, {heads}]")
+    lib = load_library()
+    if workspace is None:
+        # the caching allocator orders it with the stream, and inside a graph
+        # capture it belongs to that graph
+        size = lib.shared_prefix_workspace_bytes if prefix_pages is not None else lib.attention_workspace_bytes
+        workspace = torch.empty(size(rows, heads, requests), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    shape = (rows, heads, requests, next_n)
+    tail = (latent_pages.shape[0], max_pages, scale, softcap, _ptr(slopes), _ptr(row_positions), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel())
+    head = (_ptr(q), _ptr(latent_pages), VALUE_DTYPES[q.dtype], _ptr(block_table), _ptr(keys))
+    with torch.cuda.device(dev):
+        _arm(events, dev)
+        if sparse:
+            st = lib.sparse_attention(*head, keys.shape[1], _ptr(cu_q), *shape, *tail, _stream_ptr(dev))
+        elif prefix_pages is not None:
+            st = lib.shared_prefix_attention(*head, _ptr(starts), *shape, prefix_pages, *tail, _stream_ptr(dev))
+        else:
+            st = lib.paged_attention(*head, _ptr(starts), _ptr(cu_q), *shape, *tail, _stream_ptr(dev))
+    _check(name, st)
+
+
+def paged_attention(q, latent_pages, block_table, row_lens, next_n, scale, out, lse=None, cu_q=None, row_starts=None,
+                    softcap=0.0, slopes=None, row_positions=None, workspace=None, events=None):
+    """Attention of every row over its request's pages of the latent cache.
+
+    q [rows, heads, 576] bfloat16 or float16; latent_pages [P, 64, 576] of the
+    same type, whose first 512 dimensions are the values; block_table
+    [requests, max_pages] int32; row_lens [rows] int32: row r sees keys
+    row_starts[r] (default 0) up to row_lens[r].  next_n rows per request, or
+    next_n = 0 with cu_q [requests + 1] int32 for a ragged batch.  Scores are
+    scale q . k, then softcap * tanh(z / softcap) if softcap > 0, then minus
+    slopes[h] * |row_positions[r] - s| (default position row_lens - 1).
+    out [rows, heads, 512] of q's type; lse [rows, heads] float32 or None.  A
+    row that sees no key gets out 0 and lse -inf.
+
+    ``workspace`` is a uint8 GPU tensor of attention_workspace_bytes(rows,
+    heads, requests) bytes, allocated for the call when None; calls that share
+    one must be ordered on one stream.
+    """
+    _attention_call("paged_attention", q, latent_pages, block_table, row_lens, next_n, cu_q, row_starts, None, scale,
+                    out, lse, softcap, slopes, row_positions, workspace, events)
+
+
+def shared_prefix_attention(q, latent_pages, block_table, row_lens, next_n, prefix_pages, scale, out, lse=None,
+                            row_starts=None, softcap=0.0, slopes=None, row_positions=None, workspace=None,
+                            events=None):
+    """paged_attention for a batch whose requests' first ``prefix_pages`` pages
+    are the same (the first entries of every block_table row): their keys are
+    read once for all rows.  Workspace: shared_prefix_workspace_bytes()."""
+    _attention_call("shared_prefix_attention", q, latent_pages, block_table, row_lens, next_n, None, row_starts,
+                    prefix_pages, scale, out, lse, softcap, slopes, row_positions, workspace, events)
+
+
+def sparse_attention(q, latent_pages, block_table, indices, next_n, scale, out, lse=None, cu_q=None, softcap=0.0,
+                     slopes=None, row_positions=None, workspace=None, events=None):
+    """Attention of every row over its selected keys: indices [rows, k] int32,
+    logical key positions as topk_rows gives them (-1 padding is skipped).
+    Other arguments as for paged_attention; slopes need row_positions."""
+    _attention_call("sparse_attention", q, latent_pages, block_table, indices, next_n, cu_q, None, None, scale, out,
+                    lse, softcap, slopes, row_positions, workspace, events)
 
 
 def _read_probe(name: str, src: torch.Tensor, sink: torch.Tensor, events) -> None:

@@ -1,5 +1,7 @@
 // C ABI of the paged MQA indexer: host-side argument checks, then launches.
 // Every check runs before anything is enqueued; see paged_mqa_indexer.h.
+#include <cmath>
+
 #include "indexer_common.h"
 #include "launches.h"
 
@@ -337,6 +339,173 @@ idx_status sparse_topk(const float* scores, int64_t stride, const int32_t* hist,
   a.key_dtype = key_dtype;
   a.logits_f16 = 0;
   return from_hip(pmqa::launch_sparse_topk(a, table, kb, static_cast<hipStream_t>(stream), ev));
+}
+
+static idx_status append_call(const void* rows, int64_t row_stride, int32_t row_dim, int32_t dtype,
+                              const int32_t* positions, const int32_t* slots, const float* rope,
+                              int32_t max_positions, int32_t interleaved, int32_t tokens, int32_t num_pages,
+                              void* pages, float* k_scales, bool latent, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  if (!rows || !positions || !slots || !rope || !pages) return IDX_EINVAL;
+  if (tokens <= 0 || num_pages <= 0 || max_positions <= 0 || row_stride < row_dim) return IDX_EINVAL;
+  if (dtype != IDX_BF16 && dtype != IDX_FP16 && (latent || dtype != IDX_FP32)) return IDX_EUNSUPPORTED;
+  if (tokens > IDX_MAX_APPEND_TOKENS || num_pages > IDX_MAX_CACHE_PAGES) return IDX_EUNSUPPORTED;
+  const int64_t per16 = dtype == IDX_FP32 ? 4 : 8;  // rows are read in 16-byte pieces
+  if (row_stride > INT64_MAX / (4 * static_cast<int64_t>(tokens))) return IDX_EUNSUPPORTED;
+  if (!aligned(rows, 16) || (row_stride % per16) != 0 || !aligned(positions, 4) || !aligned(slots, 4) ||
+      !aligned(rope, 16) || !aligned(pages, 16) || (k_scales && !aligned(k_scales, 4)))
+    return IDX_EALIGN;
+  pmqa::AppendArgs a;
+  a.rows = rows;
+  a.row_stride = row_stride;
+  a.positions = positions;
+  a.slots = slots;
+  a.rope = rope;
+  a.pages = pages;
+  a.k_scales = k_scales;
+  a.dtype = dtype;
+  a.max_positions = max_positions;
+  a.interleaved = interleaved;
+  a.tokens = tokens;
+  a.num_pages = num_pages;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return from_hip(latent ? pmqa::launch_latent_append(a, s, ev) : pmqa::launch_index_k_append(a, s, ev));
+}
+
+idx_status index_k_append(const void* k, int64_t k_stride, int32_t k_dtype, const int32_t* positions,
+                          const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                          int32_t tokens, int32_t num_pages, uint8_t* kv_pages, float* k_scales, void* stream) {
+  if (!k_scales) {
+    take_events();
+    return IDX_EINVAL;
+  }
+  return append_call(k, k_stride, IDX_HEAD_DIM, k_dtype, positions, slots, rope, max_positions, interleaved, tokens,
+                     num_pages, kv_pages, k_scales, false, stream);
+}
+
+idx_status index_k_append_mxfp4(const void* k, int64_t k_stride, int32_t k_dtype, const int32_t* positions,
+                                const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                                int32_t tokens, int32_t num_pages, uint8_t* kv_pages, void* stream) {
+  return append_call(k, k_stride, IDX_HEAD_DIM, k_dtype, positions, slots, rope, max_positions, interleaved, tokens,
+                     num_pages, kv_pages, nullptr, false, stream);
+}
+
+idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const int32_t* positions,
+                         const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                         int32_t tokens, int32_t num_pages, void* latent_pages, void* stream) {
+  return append_call(kv, kv_stride, IDX_LATENT_ROW, dtype, positions, slots, rope, max_positions, interleaved, tokens,
+                     num_pages, latent_pages, nullptr, true, stream);
+}
+
+// What the three attention calls have in common; `keys` is row_lens or indices.
+static idx_status check_attention(const pmqa::AttentionArgs& a, const void* keys, size_t workspace_bytes, size_t need) {
+  if (!a.q || !a.cache || !a.block_table || !keys || !a.out || !a.workspace) return IDX_EINVAL;
+  if (a.rows <= 0 || a.heads <= 0 || a.requests <= 0 || a.num_pages <= 0 || a.max_pages <= 0 || a.next_n < 0)
+    return IDX_EINVAL;
+  if ((a.cu_q != nullptr) == (a.next_n > 0)) return IDX_EINVAL;
+  if (!a.cu_q && static_cast<int64_t>(a.requests) * a.next_n != a.rows) return IDX_EINVAL;
+  if (!std::isfinite(a.scale) || !std::isfinite(a.softcap) || a.softcap < 0.0f) return IDX_EINVAL;
+  if (a.dtype != IDX_BF16 && a.dtype != IDX_FP16) return IDX_EUNSUPPORTED;
+  if (a.rows > IDX_MAX_ROWS || a.heads > IDX_MAX_ATTENTION_HEADS || a.requests > IDX_MAX_REQUESTS ||
+      a.num_pages > IDX_MAX_CACHE_PAGES || a.max_pages > IDX_MAX_CACHE_PAGES ||
+      static_cast<int64_t>(a.requests) * a.max_pages > INT32_MAX)
+    return IDX_EUNSUPPORTED;
+  if (!aligned(a.q, 16) || !aligned(a.cache, 16) || !aligned(a.block_table, 4) || !aligned(keys, 4) ||
+      !aligned(a.cu_q, 4) || !aligned(a.row_starts, 4) || !aligned(a.row_positions, 4) || !aligned(a.slopes, 4) ||
+      !aligned(a.out, 16) || !aligned(a.lse, 4) || !aligned(a.workspace, 256))
+    return IDX_EALIGN;
+  if (workspace_bytes < need) return IDX_EWORKSPACE;
+  return IDX_OK;
+}
+
+size_t attention_workspace_bytes(int32_t rows, int32_t heads, int32_t requests) {
+  return pmqa::attention_workspace_size(rows, heads, requests);
+}
+
+size_t shared_prefix_workspace_bytes(int32_t rows, int32_t heads, int32_t requests) {
+  return pmqa::shared_prefix_workspace_size(rows, heads, requests);
+}
+
+static pmqa::AttentionArgs attention_args(const void* q, const void* latent_pages, int32_t dtype,
+                                          const int32_t* block_table, const int32_t* cu_q, int32_t rows,
+                                          int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages,
+                                          int32_t max_pages, float scale, float softcap, const float* slopes,
+                                          const int32_t* row_positions, void* out, float* lse, void* workspace) {
+  pmqa::AttentionArgs a{};
+  a.q = q;
+  a.cache = latent_pages;
+  a.block_table = block_table;
+  a.cu_q = cu_q;
+  a.row_positions = row_positions;
+  a.slopes = slopes;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.heads = heads;
+  a.requests = requests;
+  a.next_n = next_n;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  return a;
+}
+
+idx_status paged_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                           const int32_t* row_lens, const int32_t* row_starts, const int32_t* cu_q, int32_t rows,
+                           int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages,
+                           float scale, float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  pmqa::AttentionArgs a = attention_args(q, latent_pages, dtype, block_table, cu_q, rows, heads, requests, next_n,
+                                         num_pages, max_pages, scale, softcap, slopes, row_positions, out, lse,
+                                         workspace);
+  a.row_lens = row_lens;
+  a.row_starts = row_starts;
+  const idx_status st = check_attention(a, row_lens, workspace_bytes,
+                                        pmqa::attention_workspace_size(rows, heads, requests));
+  if (st != IDX_OK) return st;
+  return from_hip(pmqa::launch_paged_attention(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status shared_prefix_attention(const void* q, const void* latent_pages, int32_t dtype,
+                                   const int32_t* block_table, const int32_t* row_lens, const int32_t* row_starts,
+                                   int32_t rows, int32_t heads, int32_t requests, int32_t next_n,
+                                   int32_t prefix_pages, int32_t num_pages, int32_t max_pages, float scale,
+                                   float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  pmqa::AttentionArgs a = attention_args(q, latent_pages, dtype, block_table, nullptr, rows, heads, requests, next_n,
+                                         num_pages, max_pages, scale, softcap, slopes, row_positions, out, lse,
+                                         workspace);
+  a.row_lens = row_lens;
+  a.row_starts = row_starts;
+  a.prefix_pages = prefix_pages;
+  if (prefix_pages < 1 || prefix_pages > max_pages) return IDX_EINVAL;
+  const idx_status st = check_attention(a, row_lens, workspace_bytes,
+                                        pmqa::shared_prefix_workspace_size(rows, heads, requests));
+  if (st != IDX_OK) return st;
+  return from_hip(pmqa::launch_shared_prefix_attention(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status sparse_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                            const int32_t* indices, int32_t k, const int32_t* cu_q, int32_t rows, int32_t heads,
+                            int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages, float scale,
+                            float softcap, const float* slopes, const int32_t* row_positions, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  pmqa::AttentionArgs a = attention_args(q, latent_pages, dtype, block_table, cu_q, rows, heads, requests, next_n,
+                                         num_pages, max_pages, scale, softcap, slopes, row_positions, out, lse,
+                                         workspace);
+  a.indices = indices;
+  a.k = k;
+  if (k < 1 || k > IDX_CANDIDATE_CAPACITY || (slopes && !row_positions)) return IDX_EINVAL;
+  const idx_status st = check_attention(a, indices, workspace_bytes,
+                                        pmqa::attention_workspace_size(rows, heads, requests));
+  if (st != IDX_OK) return st;
+  return from_hip(pmqa::launch_sparse_attention(a, static_cast<hipStream_t>(stream), ev));
 }
 
 idx_status hbm_gather_probe(const uint8_t* kv_pages, const float* k_scales, const int32_t* page_list,

@@ -223,4 +223,48 @@ struct PrefillArgs {
   int32_t k_mxfp4;
 };
 
+// Cache appends: rows of `tokens` tokens, rotated by their positions, into
+// the slots (page * 64 + place) of a paged cache.
+struct AppendArgs {
+  const void* rows;          // [tokens] rows, row_stride elements apart
+  int64_t row_stride;
+  const int32_t* positions;  // [tokens]
+  const int32_t* slots;      // [tokens], negative: not written
+  const float* rope;         // [max_positions][64]: 32 cosines, 32 sines
+  void* pages;
+  float* k_scales;           // FP8 index keys only
+  int32_t dtype;
+  int32_t max_positions;
+  int32_t interleaved;
+  int32_t tokens;
+  int32_t num_pages;
+};
+
+// Attention over the latent cache [num_pages][64][576].
+struct AttentionArgs {
+  const void* q;                 // [rows][heads][576]
+  const void* cache;
+  const int32_t* block_table;    // [requests][max_pages]
+  const int32_t* cu_q;           // [requests + 1], or null: next_n rows per request
+  const int32_t* row_lens;       // [rows] end of the keys (dense)
+  const int32_t* row_starts;     // [rows] first key, or null: 0 (dense)
+  const int32_t* row_positions;  // [rows] position the bias counts from, or null: row_lens - 1
+  const int32_t* indices;        // [rows][k] selected keys (sparse)
+  const float* slopes;           // [heads], or null: no bias
+  void* out;                     // [rows][heads][512]
+  float* lse;                    // [rows][heads], or null
+  void* workspace;
+  float scale;
+  float softcap;                 // 0: none
+  int32_t dtype;
+  int32_t rows;
+  int32_t heads;
+  int32_t requests;
+  int32_t next_n;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t k;
+  int32_t prefix_pages;
+};
+
 }  // namespace pmqa

@@ -52,4 +52,13 @@ hipError_t launch_hbm_gather_probe(const uint8_t* pool, const float* scales, con
 hipError_t launch_mfma_valu_probe(int mode, int workgroups, int iters, float* out, hipStream_t stream,
                                   LaunchEvents ev = {});
 
+hipError_t launch_index_k_append(const AppendArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_latent_append(const AppendArgs& a, hipStream_t stream, LaunchEvents ev = {});
+
+size_t attention_workspace_size(int32_t rows, int32_t heads, int32_t requests);
+size_t shared_prefix_workspace_size(int32_t rows, int32_t heads, int32_t requests);
+hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_shared_prefix_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_sparse_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
+
 }  // namespace pmqa
