@@ -24,6 +24,7 @@
 // order.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "indexer_common.h"
 #include "launches.h"
@@ -36,43 +37,50 @@ constexpr int kValDim = IDX_LATENT_DIM;            // 512
 constexpr int kRowBytes = kRowDim * 2;             // 1152
 constexpr int kKSteps = kRowDim / 32;              // 18 MFMA steps of S
 constexpr int kDimTiles = kValDim / 16;            // 32 output tiles of 16 dimensions
-constexpr int kTile = 64;                          // keys per iteration of a workgroup
-constexpr int kBlkBytes = 16 * kRowBytes;          // 16 keys in LDS: 18432
-constexpr int kSlotBytes = kTile * kRowBytes;      // 73728
-constexpr int kSlots = 2;
+constexpr int kTile = 64;                          // keys per entry of the work list
+constexpr int kOctBytes = 8 * kRowBytes;           // 8 keys in LDS: 9216
+constexpr int kBlkBytes = 2 * kOctBytes;           // 16 keys
+constexpr int kRingBytes = 2 * kTile * kRowBytes;  // 147456: 128 keys in all slots together
+constexpr int kWindow = 2048;                      // sparse: keys whose cache rows are resolved at a time
 constexpr int kAttnThreads = 256;
-constexpr int kChunkDims = 128;                    // epilogue: dimensions exchanged at a time
-constexpr int kChunkStride = kChunkDims + 4;       // floats; the pad spreads the pairs over all banks
 constexpr int kScanChunks = 1056;                  // work-list chunks of 256 pair tiles
 constexpr float kMInit = -1.7e38f;                 // running maximum before any key (finite: no inf - inf)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum is raised only when a score passes it by more than this
-// (powers of two): P then holds values up to 2^6, exact in the final quotient,
-// and the 128 accumulators are rescaled a few times per row instead of at
-// every new maximum.
-constexpr float kRaise = 6.0f;
-
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // P is rounded to the cache's 16-bit type for the second product (an MFMA
 // takes both operands in one type): a relative error of at most half a step
 // per key, independent over the keys, so it stays below the rounding of the
-// output itself; l sums the unrounded values.  FP16 has few exponents, so its
-// P is scaled by 2^8 (kShift): keys 2^-22 below the maximum are still normal.
+// output itself; l sums the unrounded values.
+//
+// The running maximum is raised only when a score passes it by more than
+// kRaise (powers of two): until then P holds values above 1, exact in the final
+// quotient, and the accumulators need not be rescaled.  BF16 and float32 have
+// exponents for 2^60 (and 2^60 times a sum of 2^31 keys), so there a second
+// maximum hardly ever comes up.  FP16 ends at 2^16; its P is scaled by 2^8
+// (kShift), so that weights down to 2^-22 of the maximum are still normal.
 template <int DT>
 struct Elem;
 template <>
 struct Elem<IDX_BF16> {
-  static constexpr float kShift = 0.0f;
+  static constexpr float kShift = 0.0f, kRaise = 60.0f;
   static __device__ __forceinline__ f32x4 mfma32(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma_wide(s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  static __device__ __forceinline__ void mfma_acc(s16x8 a, s16x8 b, f32x16& c) {
+    __asm__ volatile("s_nop 1\nv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ f32x4 mfma16(s16x4 a, s16x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
@@ -83,10 +91,17 @@ struct Elem<IDX_BF16> {
 };
 template <>
 struct Elem<IDX_FP16> {
-  static constexpr float kShift = 8.0f;
+  static constexpr float kShift = 8.0f, kRaise = 6.0f;
   static __device__ __forceinline__ f32x4 mfma32(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
+  }
+  static __device__ __forceinline__ f32x16 mfma_wide(s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+  static __device__ __forceinline__ void mfma_acc(s16x8 a, s16x8 b, f32x16& c) {
+    __asm__ volatile("s_nop 1\nv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ f32x4 mfma16(s16x4 a, s16x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
@@ -97,48 +112,67 @@ struct Elem<IDX_FP16> {
   }
 };
 
+// mfma_acc: the 256 accumulators of a wide wave take exactly the accumulation
+// registers, the queries and everything else the 256 vector registers; written
+// out, the instruction leaves the compiler no other choice (left to itself it
+// moves operands between the two files at every step).  The two wait states
+// cover an operand that a vector instruction has just written (they pass while
+// the MFMA before is still running); before vector instructions read an
+// accumulator, settle() lets the last MFMA finish.
+__device__ __forceinline__ void settle(f32x16& c) { __asm__ volatile("s_nop 15\ns_nop 7" : "+a"(c)); }
+
+// No instruction: keeps an accumulator in its registers where control flow
+// joins (a value that every reader takes from the accumulation registers is
+// not moved out of them).
+__device__ __forceinline__ void pin(f32x16& c) { __asm__ volatile("" : "+a"(c)); }
+
 // Where invalid keys are read from: a row of zeros, so that neither S nor the
 // value product meets what the cache holds there.
 __device__ __attribute__((aligned(128))) const uint32_t kZeroRow[kRowBytes / 4] = {};
 
-// LDS image of 16 keys (18 KiB): nine 1 KiB pieces per 8 keys, a piece holding
-// 128 bytes of each of them -- what one direct-to-LDS load of 64 x 16 bytes
-// writes.  Within its 128 bytes a key's 16-byte chunks are exchanged by
-// c ^ swz(key), which spreads both kinds of reads over all banks: the K
-// operand (16 keys, one chunk) and the transposed V operand (8 keys of one
-// parity class, two neighbouring chunks).
-__device__ __forceinline__ int swz(int key) { return (((key >> 1) & 3) << 1) | ((key >> 3) & 1); }
-__device__ __forceinline__ int key_offset(int key) { return (key >> 3) * (kBlkBytes / 2) + (key & 7) * 128; }
+// LDS image of 8 keys (9 KiB): nine 1 KiB pieces, each holding 128 bytes of
+// every key -- what one direct-to-LDS load of 64 x 16 bytes writes.  Within
+// its 128 bytes a key's 16-byte chunks are exchanged by c ^ swz(key), which
+// spreads every kind of read over all 64 banks: the 128-bit reads of the K
+// operand (served 16 lanes at a time, in groups 0-3, 12-15, 20-23, 24-27 and
+// 4-7, 8-11, 16-19, 28-31 of each half wave) for 16 keys by 4 chunks and for 32
+// keys by 2, and the transposing 64-bit reads of V (half a wave at a time) for
+// 8 keys by 2 chunks and for 4 keys by 4.  Measured: 245 and 226 bytes a clock
+// and CU, against 125 for the first with the chunks exchanged by bits 1-3 of
+// the key.
+__device__ __forceinline__ int swz(int key) { return (((key >> 1) & 1) << 2) | (-(key >> 2) & 3); }
+__device__ __forceinline__ int key_offset(int key) { return (key >> 3) * kOctBytes + (key & 7) * 128; }
 
-// Issues this wave's 16 keys of a tile into LDS: lane l reads 16-byte pieces of
-// keys l / 8 and 8 + l / 8 from the addresses a0 and a1.  The instruction's
-// offset advances both the source and the LDS address by 128; M0 supplies the
-// rest of the 1 KiB step.  Written in assembly so that the compiler does not
-// drain the loads in flight before every LDS access of the other slot; the
-// caller waits (vmcnt) before the barrier that publishes the tile.
-__device__ __forceinline__ void load_keys(const char* a0, const char* a1, uint32_t lds) {
-  constexpr uint32_t kStep = 1024 - 128;
-#define PMQA_LOAD(v, j, at)                      \
-  "s_add_u32 m0, %[l], " at "\n"                 \
-  "s_nop 0\n"                                    \
-  "global_load_lds_dwordx4 %[" v "], off offset:" j "\n"
-  static_assert(kStep == 896, "offsets below are multiples of 896");
+// Issues 8 keys into LDS: lane l reads 16-byte pieces of key l / 8 from `at`.
+// The instruction's offset advances both the source and the LDS address by
+// 128; M0 supplies the rest of the 1 KiB step.  Written in assembly so that
+// the compiler does not drain the loads in flight before every LDS access of
+// the other slots; the caller waits (vmcnt) before the barrier that publishes
+// the keys.
+constexpr int kOctLoads = 9;
+__device__ __forceinline__ void load_octet(const char* at, uint32_t lds) {
+#define PMQA_LOAD(j, m)             \
+  "s_add_u32 m0, %[l], " m "\n"     \
+  "s_nop 0\n"                       \
+  "global_load_lds_dwordx4 %[a], off offset:" j "\n"
   __asm__ volatile(
-      PMQA_LOAD("a", "0", "0") PMQA_LOAD("a", "128", "896") PMQA_LOAD("a", "256", "1792")
-      PMQA_LOAD("a", "384", "2688") PMQA_LOAD("a", "512", "3584") PMQA_LOAD("a", "640", "4480")
-      PMQA_LOAD("a", "768", "5376") PMQA_LOAD("a", "896", "6272") PMQA_LOAD("a", "1024", "7168")
-      PMQA_LOAD("b", "0", "9216") PMQA_LOAD("b", "128", "10112") PMQA_LOAD("b", "256", "11008")
-      PMQA_LOAD("b", "384", "11904") PMQA_LOAD("b", "512", "12800") PMQA_LOAD("b", "640", "13696")
-      PMQA_LOAD("b", "768", "14592") PMQA_LOAD("b", "896", "15488") PMQA_LOAD("b", "1024", "16384")
+      PMQA_LOAD("0", "0") PMQA_LOAD("128", "896") PMQA_LOAD("256", "1792") PMQA_LOAD("384", "2688")
+      PMQA_LOAD("512", "3584") PMQA_LOAD("640", "4480") PMQA_LOAD("768", "5376") PMQA_LOAD("896", "6272")
+      PMQA_LOAD("1024", "7168")
       :
-      : [l] "s"(lds), [a] "v"(a0), [b] "v"(a1)
+      : [l] "s"(lds), [a] "v"(at)
       : "memory", "m0", "scc");
 #undef PMQA_LOAD
 }
 
-__device__ __forceinline__ void wait_all_and_barrier() {
+// Waits until at most LEFT vector memory operations of this wave are
+// outstanding, then for the other waves; LDS accesses on both sides keep their
+// sides.
+template <int LEFT>
+__device__ __forceinline__ void wait_and_barrier() {
   __asm__ volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0); the compiler counts its own loads as done, too
+  // lgkmcnt(0), vmcnt(LEFT): the counter's two fields
+  __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | ((LEFT >> 4) << 14));
   __builtin_amdgcn_s_barrier();
   __asm__ volatile("" ::: "memory");
 }
@@ -150,16 +184,21 @@ __device__ __forceinline__ s16x4 lds_read_tr(uint32_t at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<LdsVec4>(at));
 }
 
-// Maximum of a value over the four lanes (l, l ^ 16, l ^ 32, l ^ 48) of a pair.
+// Maximum and sum of a value over the lanes of a pair: l, l ^ 16, l ^ 32 and
+// l ^ 48, or (WIDE) l and l ^ 32.
+template <bool WIDE>
 __device__ __forceinline__ float pair_max(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  if constexpr (WIDE) return x;
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+template <bool WIDE>
 __device__ __forceinline__ float pair_sum(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  if constexpr (WIDE) return x;
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
@@ -345,14 +384,19 @@ __host__ __device__ __forceinline__ int64_t item_count(const AttentionArgs& a) {
 
 // The workgroup's share [t0, t1) of the tile list and the item it starts in.
 struct Share {
-  int64_t t0, t1;      // tiles
+  int64_t t0, t1;      // units
   int64_t total;
-  int64_t item_at;     // tile offset of `item`
+  int64_t item_at;     // unit offset of `item`
   int item;
   int groups;          // workgroups with work
 };
 
-// Share of workgroup w: as many groups as give each kMinTiles tiles.
+// Taking up a pair tile and writing it costs about as much as kItemCost tiles
+// of keys: a pair tile counts for that many more, at its beginning.
+constexpr int kItemCost = 3;
+__device__ __forceinline__ int item_units(const Item& it) { return it.tiles ? it.tiles + kItemCost : 0; }
+
+// Share of workgroup w: as many groups as give each min_units.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int groups, int w) {
   return total * w / groups;
 }
@@ -365,15 +409,15 @@ __device__ __forceinline__ int share_owner(int64_t total, int groups, int64_t t)
 }
 
 template <int KIND, int M>
-__device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_tiles, int* s_scan, int64_t* s_res) {
+__device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_units, int* s_scan, int64_t* s_res) {
   Share s;
   const int items = static_cast<int>(item_count<KIND, M>(a));
   const int tid = threadIdx.x;
   if constexpr (KIND == kSparse) {
     if (!a.cu_q) {
-      const int n = (a.k + kTile - 1) / kTile;
+      const int n = (a.k + kTile - 1) / kTile + kItemCost;
       s.total = static_cast<int64_t>(items) * n;
-      s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_tiles)));
+      s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_units)));
       s.t0 = w < s.groups ? share_begin(s.total, s.groups, w) : 0;
       s.t1 = w < s.groups ? share_begin(s.total, s.groups, w + 1) : 0;
       s.item = static_cast<int>(s.t0 / n);
@@ -386,9 +430,10 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_til
   const int chunks = (items + kAttnThreads - 1) / kAttnThreads;
   int* s_wave = s_scan;
   int* s_chunk = s_scan + kAttnThreads / kWave;
+  int n = 0;
   for (int c = 0; c < chunks; ++c) {
     const int id = c * kAttnThreads + tid;
-    const int n = id < items ? make_item<KIND, M, 1>(a, id).tiles : 0;
+    n = id < items ? item_units(make_item<KIND, M, 1>(a, id)) : 0;
     const int sum = wave_sum(n);
     if (lane_id() == 0) s_wave[tid / kWave] = sum;
     __syncthreads();
@@ -398,7 +443,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_til
   int64_t total = 0;
   for (int c = 0; c < chunks; ++c) total += s_chunk[c];
   s.total = total;
-  s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), total / min_tiles)));
+  s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), total / min_units)));
   if (w >= s.groups || total == 0) {
     s.t0 = s.t1 = 0;
     s.item = 0;
@@ -411,7 +456,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_til
   int c = 0;
   while (c + 1 < chunks && at + s_chunk[c] <= s.t0) at += s_chunk[c++];
   const int id = c * kAttnThreads + tid;
-  const int n = id < items ? make_item<KIND, M, 1>(a, id).tiles : 0;
+  if (c + 1 < chunks) n = id < items ? item_units(make_item<KIND, M, 1>(a, id)) : 0;
   const int upto = wave_inclusive_scan(n);
   if (lane_id() == kWave - 1) s_wave[tid / kWave] = upto;
   __syncthreads();
@@ -444,331 +489,546 @@ struct alignas(16) JoinInfo {
 // piece, w + item -- consecutive over a pair tile's workgroups.
 __host__ __device__ __forceinline__ int64_t piece_floats(int m) { return static_cast<int64_t>(m) * (kValDim + 2); }
 
-template <int DT, int KIND, int PT, int PG>
-__global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArgs a, int min_tiles, JoinInfo* join,
+// How a workgroup of four waves divides a pair tile of M pairs and a step of
+// keys.  Narrow (M <= 64): 16 pairs per wave, 64 keys per step in 2 slots, and
+// where fewer than four waves cover the pairs the others take other keys of
+// the same pairs (streams, joined at the end); their time is the K stream's.
+// Wide (M = 128): 32 pairs per wave, so that each LDS operand feeds twice the
+// arithmetic, and 32 keys per step in 4 slots: the value product of a step
+// runs while the next step's softmax is computed, two steps of loads ahead.
+template <int M>
+struct Shape {
+  static constexpr bool kWide = M == 128;
+  static constexpr int kWavePairs = kWide ? 32 : 16;
+  static constexpr int kGroups = M / kWavePairs;      // waves that cover the pairs
+  static constexpr int kStreams = 4 / kGroups;
+  static constexpr int kKeys = kWide ? 32 : 64;       // keys of a step
+  static constexpr int kSlots = 128 / kKeys;
+  static constexpr int kSlotBytes = kKeys * kRowBytes;
+  static constexpr int kDistance = kWide ? 2 : 1;     // steps that are loaded ahead
+  static constexpr int kOctets = kKeys / 32;          // octets that each wave loads per step
+  static constexpr int kBlocks = kWide ? 2 : kKeys / 16 / kStreams;  // 16-key blocks of a step per wave
+};
+
+template <int DT, int KIND, int M>
+__global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArgs a, int min_units, JoinInfo* join,
                                                                     float* pieces) {
   using E = Elem<DT>;
-  constexpr int kWavePairs = 16 * PT;           // pairs of a wave
-  constexpr int M = kWavePairs * PG;            // pairs of the workgroup
-  constexpr int TS = 4 / PG;                    // key streams: waves that take different keys of the same pairs
-  constexpr int ST = 4 / TS;                    // 16-key blocks of a tile per wave
-  __shared__ __attribute__((aligned(1024))) char s_keys[kSlots * kSlotBytes];
-  __shared__ int s_tok[kSlots][kTile];          // sparse: logical key of every tile row, -1 for none
-  __shared__ float2 s_ml[4][kWavePairs];
+  using S = Shape<M>;
+  constexpr int kStepsPerTile = kTile / S::kKeys;
+  constexpr int ST = S::kBlocks;
+  __shared__ __attribute__((aligned(1024))) char s_keys[kRingBytes];
+  __shared__ int s_rows[KIND == kSparse ? kWindow : 1];       // sparse: cache row of each listed key, -1: none
+  __shared__ uint32_t s_live[S::kSlots][4];                   // sparse: bits of the keys that are there
+  __shared__ float2 s_ml[4][S::kWavePairs];
   __shared__ int64_t s_res[2];
-  __shared__ int s_scan[kAttnThreads / kWave + kScanChunks];
+  __shared__ int s_scan[KIND == kSparse ? 8 + 640 : kAttnThreads / kWave + kScanChunks];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grid = gridDim.x;
   // consecutive shares on one XCD (workgroups are dealt to the 8 XCDs in turn)
   const int w = (grid & 7) ? static_cast<int>(blockIdx.x)
                            : static_cast<int>(blockIdx.x & 7) * (grid >> 3) + static_cast<int>(blockIdx.x >> 3);
-  const Share share = find_share<KIND, M>(a, w, grid, min_tiles, s_scan, s_res);
+  const Share share = find_share<KIND, M>(a, w, grid, min_units, s_scan, s_res);
   if (KIND != kShared && tid == 0) join[w].pieces = 0;
   if (share.t0 >= share.t1) return;
 
-  const uint32_t keys_lds = static_cast<uint32_t>(
+  const uint32_t ring = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)s_keys));
-  const int pg = wave / TS, ts = wave % TS;
-  const int n16 = lane & 15, g4 = lane >> 4;
-  // this lane's places in a 16-key block: K operand (key n16, chunk g4), and
-  // the transposed V operand (key 4 g4 + n16 / 4, 4 dimensions n16 % 4)
-  const uint32_t k_at = key_offset(n16) + ((g4 ^ swz(n16)) * 16);
-  const int vkey = 4 * g4 + (n16 >> 2);
-  const uint32_t v_at = key_offset(vkey) + ((((n16 >> 1) & 1) ^ swz(vkey)) * 16) + (n16 & 1) * 8;
-  const int src0 = ((lane & 7) ^ swz(lane >> 3)) * 16;        // source chunk of the keys lane / 8 ...
-  const int src1 = ((lane & 7) ^ swz(8 + (lane >> 3))) * 16;  // ... and 8 + lane / 8
+  const int pg = wave / S::kStreams, ts = wave % S::kStreams;
+  const int n16 = lane & 15, g4 = lane >> 4, half = lane >> 5;
+  const int col = lane & (S::kWavePairs - 1);  // this lane's pair of the wave's
+  // places of this lane in a step's keys: K operand and transposed V operand
+  uint32_t k_at, v_at;
+  if constexpr (S::kWide) {
+    const int key = lane & 31, vkey = 4 * half + (n16 >> 2);
+    k_at = key_offset(key) + (half ^ swz(key)) * 16;
+    v_at = key_offset(vkey) + (((2 * (g4 & 1) + ((lane & 3) >> 1)) ^ swz(vkey)) * 16) + (lane & 1) * 8;
+  } else {
+    const int vkey = 4 * g4 + (n16 >> 2);
+    k_at = key_offset(n16) + (g4 ^ swz(n16)) * 16;
+    v_at = key_offset(vkey) + (((n16 >> 1) & 1) ^ swz(vkey)) * 16 + (n16 & 1) * 8;
+  }
   const int capacity = a.max_pages * kPage;
   const char* cache = static_cast<const char*>(a.cache);
   const float to_log2 = a.scale * kLog2e;
 
+  const int items = static_cast<int>(item_count<KIND, M>(a));
   int64_t at = share.t0;
   int64_t item_at = share.item_at;
   int item = share.item;
-  const int items = static_cast<int>(item_count<KIND, M>(a));
-  while (at < share.t1 && item < items) {
+  for (; at < share.t1 && item < items; ++item) {
     const Item it = make_item<KIND, M, kWave>(a, item);
-    if (it.tiles == 0 || item_at + it.tiles <= at) {  // no pairs: nothing to do or to write
-      item_at += it.tiles;
-      ++item;
-      continue;
-    }
-    const int lo = static_cast<int>(at - item_at);
-    const int hi = static_cast<int>(min(static_cast<int64_t>(it.tiles), share.t1 - item_at));
+    const int64_t tiles_at = item_at + (it.tiles ? kItemCost : 0);
+    item_at += item_units(it);
+    const int lo = static_cast<int>(max(int64_t{0}, at - tiles_at));
+    const int hi = static_cast<int>(min(static_cast<int64_t>(it.tiles), share.t1 - tiles_at));
+    at = item_at;
+    if (lo >= hi) continue;  // no pairs, or another workgroup's keys
     const bool whole = lo == 0 && hi == it.tiles && KIND != kShared;
     const int32_t* table = a.block_table + static_cast<int64_t>(it.request) * a.max_pages;
+    const int step0 = lo * kStepsPerTile, step_end = hi * kStepsPerTile;
 
-    // the pairs of this lane: queries in the B operand's layout
-    s16x8 q[PT][kKSteps];
-    int p_start[PT], p_end[PT], p_pos[PT];
-    float p_slope[PT];
-#pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
-      const int local = min(pg * kWavePairs + pt * 16 + n16, it.pairs - 1);
-      const int pair = it.pair0 + local;
-      const int row = it.row0 + pair / a.heads;
-      const char* qp = static_cast<const char*>(a.q) +
-                       (static_cast<int64_t>(it.row0) * a.heads + pair) * kRowBytes + g4 * 16;
-#pragma unroll
-      for (int ks = 0; ks < kKSteps; ++ks) q[pt][ks] = *reinterpret_cast<const s16x8*>(qp + ks * 64);
-      p_start[pt] = 0;
-      p_end[pt] = capacity;
-      if constexpr (KIND != kSparse) {
-        p_end[pt] = clamp_len(a.row_lens[row], capacity);
-        if (a.row_starts) p_start[pt] = max(0, a.row_starts[row]);
-      }
-      p_slope[pt] = a.slopes ? a.slopes[pair % a.heads] * kLog2e : 0.0f;
-      p_pos[pt] = a.row_positions ? a.row_positions[row] : p_end[pt] - 1;
-      p_start[pt] = max(p_start[pt], it.key_lo);
-      p_end[pt] = min(p_end[pt], it.key_hi);
-    }
-
-    // ---- loading: this wave's 16 keys of tile `t` (counted from the item's first)
+    // ---- loading
     int page_window = -1, window_page = 0;  // dense: page ids of 64 tiles, one per lane
-    int next_tok0 = -1, next_tok1 = -1;     // sparse: keys of the tile to be issued next ...
-    int next_page0 = 0, next_page1 = 0;     // ... and their pages
-    int after_tok0 = -1, after_tok1 = -1;   // keys of the tile after it
-    auto fetch_tokens = [&](int t, int& tok0, int& tok1) {
-      const int c0 = t * kTile + wave * 16 + (lane >> 3);
-      const int32_t* list = a.indices + static_cast<int64_t>(it.row0) * a.k;
-      tok0 = c0 < a.k ? list[c0] : -1;
-      tok1 = c0 + 8 < a.k ? list[c0 + 8] : -1;
-      if (tok0 >= capacity) tok0 = -1;
-      if (tok1 >= capacity) tok1 = -1;
+    int row_window = -1;                    // sparse: window of keys in s_rows
+    // sparse: cache rows of kWindow listed keys, two dependent loads for all of them at once
+    auto resolve = [&](int window) {
+      row_window = window;
+      const int32_t* list = a.indices + static_cast<int64_t>(it.row0) * a.k + window * kWindow;
+      const int n = min(kWindow, a.k - window * kWindow);
+      int tok[kWindow / kAttnThreads];
+#pragma unroll
+      for (int i = 0; i < kWindow / kAttnThreads; ++i) {
+        const int c = i * kAttnThreads + tid;
+        tok[i] = c < n ? list[c] : -1;
+      }
+      int page[kWindow / kAttnThreads];
+#pragma unroll
+      for (int i = 0; i < kWindow / kAttnThreads; ++i) {
+        if (tok[i] >= capacity) tok[i] = -1;
+        page[i] = tok[i] >= 0 ? table[tok[i] / kPage] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kWindow / kAttnThreads; ++i)
+        s_rows[i * kAttnThreads + tid] =
+            tok[i] >= 0 ? max(0, min(page[i], a.num_pages - 1)) * kPage + (tok[i] & (kPage - 1)) : -1;
     };
-    auto fetch_pages = [&](int tok0, int tok1, int& page0, int& page1) {
-      page0 = table[max(tok0, 0) / kPage];
-      page1 = table[max(tok1, 0) / kPage];
-    };
-    auto issue = [&](int t, int slot) {
-      int slot0, slot1;      // cache rows
-      bool live0, live1;
+    const char* zero = reinterpret_cast<const char*>(kZeroRow);
+    auto issue = [&](int step) {
+      const int slot = (step - step0) & (S::kSlots - 1);
+      int page = 0;
+      const int key0 = step * S::kKeys + wave * (8 * S::kOctets);  // this wave's first key of the item's list
       if constexpr (KIND == kSparse) {
-        live0 = next_tok0 >= 0;
-        live1 = next_tok1 >= 0;
-        slot0 = max(0, min(next_page0, a.num_pages - 1)) * kPage + (max(next_tok0, 0) & (kPage - 1));
-        slot1 = max(0, min(next_page1, a.num_pages - 1)) * kPage + (max(next_tok1, 0) & (kPage - 1));
-        if ((lane & 7) == 0) {
-          s_tok[slot][wave * 16 + (lane >> 3)] = live0 ? next_tok0 : -1;
-          s_tok[slot][wave * 16 + 8 + (lane >> 3)] = live1 ? next_tok1 : -1;
+        if (key0 / kWindow != row_window) {  // the same for all waves: a window is whole steps
+          lds_barrier();
+          resolve(key0 / kWindow);
+          lds_barrier();
         }
       } else {
-        const int tile = it.tile0 + t;
+        const int tile = it.tile0 + key0 / kTile;
         if ((tile >> 6) != page_window) {
           page_window = tile >> 6;
           window_page = table[min(page_window * 64 + lane, a.max_pages - 1)];
         }
-        const int page = max(0, min(__builtin_amdgcn_readlane(window_page, tile & 63), a.num_pages - 1));
-        const int key = wave * 16 + (lane >> 3);
-        slot0 = page * kPage + key;
-        slot1 = slot0 + 8;
-        // keys that no row of the pair tile sees are not read
-        live0 = tile * kTile + key >= it.min_start && tile * kTile + key < it.max_end;
-        live1 = tile * kTile + key + 8 >= it.min_start && tile * kTile + key + 8 < it.max_end;
+        page = max(0, min(__builtin_amdgcn_readlane(window_page, tile & 63), a.num_pages - 1));
       }
-      const char* zero = reinterpret_cast<const char*>(kZeroRow);
-      const char* a0 = (live0 ? cache + static_cast<int64_t>(slot0) * kRowBytes : zero) + src0;
-      const char* a1 = (live1 ? cache + static_cast<int64_t>(slot1) * kRowBytes : zero) + src1;
-      if constexpr (KIND == kSparse) {
-        // two dependent loads run ahead of each tile: its key ids two issues
-        // early, their pages one issue early, so that neither is waited for
-        // (and none is waited for with this tile's loads in flight)
-        next_tok0 = after_tok0;
-        next_tok1 = after_tok1;
-        fetch_pages(next_tok0, next_tok1, next_page0, next_page1);
-        fetch_tokens(t + 2, after_tok0, after_tok1);
+      uint32_t live_bits = 0;
+#pragma unroll
+      for (int o = 0; o < S::kOctets; ++o) {
+        const int key = key0 + 8 * o + (lane >> 3);
+        int row;
+        bool live;
+        if constexpr (KIND == kSparse) {
+          row = s_rows[key & (kWindow - 1)];
+          live = row >= 0;
+          const uint64_t mask = __ballot(live);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) live_bits |= static_cast<uint32_t>(mask >> (8 * i) & 1) << (8 * o + i);
+        } else {
+          // keys that no row of the pair tile sees are not read
+          const int tok = it.tile0 * kTile + key;
+          row = page * kPage + (key & (kPage - 1));
+          live = tok >= it.min_start && tok < it.max_end;
+        }
+        const char* from = (live ? cache + static_cast<int64_t>(row) * kRowBytes : zero) +
+                           (((lane & 7) ^ swz((8 * ((wave * S::kOctets + o) & 1)) + (lane >> 3))) * 16);
+        load_octet(from, ring + slot * S::kSlotBytes + (wave * S::kOctets + o) * kOctBytes);
       }
-      load_keys(a0, a1, keys_lds + slot * kSlotBytes + wave * kBlkBytes);
+      if (KIND == kSparse && lane == 0) s_live[slot][wave] = live_bits;
     };
 
-    f32x4 acc[PT][kDimTiles];
-    float m[PT], l[PT];
+    // ---- the queries come through the ring as well (whole 128-byte pieces; the
+    // operand layout's own addresses would take a quarter of each line), in
+    // the last slots, beside the first keys where there is room
+    constexpr int kQ = S::kWide ? 36 : kKSteps;
+    const uint32_t q_ring = ring + kRingBytes - M * kRowBytes;
+    const int64_t pair_base = static_cast<int64_t>(it.row0) * a.heads + it.pair0;  // over the whole batch
+    lds_barrier();  // the previous item's epilogue has left the ring
+    for (int o = wave; o < M / 8; o += 4) {
+      const int pair = 8 * o + (lane >> 3);
+      const char* from = (pair < it.pairs ? static_cast<const char*>(a.q) + (pair_base + pair) * kRowBytes : zero) +
+                         (((lane & 7) ^ swz(pair & 15)) * 16);
+      load_octet(from, q_ring + o * kOctBytes);
+    }
+    int p_start = 0, p_end = capacity, p_pos;
+    float p_slope;
+    {
+      const int pair = it.pair0 + min(pg * S::kWavePairs + col, it.pairs - 1);
+      const int row = it.row0 + pair / a.heads;
+      if constexpr (KIND != kSparse) {
+        p_end = clamp_len(a.row_lens[row], capacity);
+        if (a.row_starts) p_start = max(0, a.row_starts[row]);
+      }
+      p_slope = a.slopes ? a.slopes[pair % a.heads] * kLog2e : 0.0f;
+      p_pos = a.row_positions ? a.row_positions[row] : p_end - 1;
+      p_start = max(p_start, it.key_lo);
+      p_end = min(p_end, it.key_hi);
+    }
+    if constexpr (KIND == kSparse) {
+      resolve(step0 * S::kKeys / kWindow);
+      lds_barrier();
+    }
+    // narrow: slot 0 holds step0's keys, slot 1 the queries
+    if constexpr (!S::kWide) issue(step0);
+    wait_and_barrier<0>();
+    s16x8 q[kQ];
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
-      m[pt] = kMInit;
-      l[pt] = 0.0f;
+    for (int ks = 0; ks < kQ; ++ks) {
+      if constexpr (S::kWide)
+        q[ks] = lds_read(q_ring + pg * 32 * kRowBytes + (k_at ^ ((ks & 3) * 32)) + (ks >> 2) * 1024);
+      else
+        q[ks] = lds_read(q_ring + pg * 16 * kRowBytes + (k_at ^ ((ks & 1) * 64)) + (ks >> 1) * 1024);
+    }
+    lds_barrier();
+    if constexpr (S::kWide) {
 #pragma unroll
-      for (int d = 0; d < kDimTiles; ++d) acc[pt][d] = f32x4{0, 0, 0, 0};
+      for (int d = 0; d < S::kDistance; ++d)
+        if (step0 + d < step_end) issue(step0 + d);
     }
 
-    __syncthreads();  // the slots are free (the previous item's epilogue used them)
-    if constexpr (KIND == kSparse) {
-      fetch_tokens(lo, next_tok0, next_tok1);
-      fetch_tokens(lo + 1, after_tok0, after_tok1);
-      fetch_pages(next_tok0, next_tok1, next_page0, next_page1);
-    }
-    issue(lo, 0);
-    for (int t = lo; t < hi; ++t) {
-      const int slot = (t - lo) & 1;
-      wait_all_and_barrier();  // tile t is in its slot, and every wave has left the other one
-      if (t + 1 < hi) issue(t + 1, slot ^ 1);
-      const uint32_t blk0 = keys_lds + slot * kSlotBytes + ts * ST * kBlkBytes;
+    // accumulators: dimensions on the rows, pairs on the columns
+    using Acc = std::conditional_t<S::kWide, f32x16, f32x4>;
+    constexpr int kAccs = S::kWide ? kValDim / 32 : kDimTiles;
+    constexpr int kScores = ST * (S::kWide ? 8 : 4);  // scores of this lane per step
+    Acc acc[kAccs];
+#pragma unroll
+    for (int d = 0; d < kAccs; ++d) acc[d] = Acc{};
+    float m = kMInit, l = 0.0f;
+    s16x8 p_wide[2] = {};  // wide: weights of the step before
+
+    // the value product of one step (wide), V^T P^T on the keys at `base`; each
+    // of the 16 dimension tiles is followed by a piece of other work, and the
+    // operands are read four tiles ahead
+    auto value_wide = [&](uint32_t base, auto&& between) {
+      if constexpr (S::kWide) {
+        constexpr int kRing = 5;
+        s16x8 v[kRing][2];
+        auto read = [&](int d) {
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            const uint32_t va = base + (v_at ^ ((d & 1) * 64)) + (2 * kk) * kOctBytes + (d >> 1) * 1024;
+            const uint32_t vb = base + (v_at ^ ((d & 1) * 64) ^ 32) + (2 * kk + 1) * kOctBytes + (d >> 1) * 1024;
+            v[d % kRing][kk] = __builtin_shufflevector(lds_read_tr(va), lds_read_tr(vb), 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+        };
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < kRing - 1; ++d) read(d);
+#pragma unroll
+        for (int d = 0; d < kAccs; d += 2) {
+          __builtin_amdgcn_sched_barrier(0);
+          E::mfma_acc(v[d % kRing][0], p_wide[0], acc[d]);
+          if (d + kRing - 1 < kAccs) read(d + kRing - 1);
+          between(d);
+          __builtin_amdgcn_sched_barrier(0);
+          E::mfma_acc(v[(d + 1) % kRing][0], p_wide[0], acc[d + 1]);
+          E::mfma_acc(v[d % kRing][1], p_wide[1], acc[d]);
+          between(d + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          E::mfma_acc(v[(d + 1) % kRing][1], p_wide[1], acc[d + 1]);
+          if (d + kRing < kAccs) read(d + kRing);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+
+    // One step.  Returns whether the accumulators of a wide wave have to take a
+    // raised maximum; they do outside the step, so that inside it nothing but
+    // the MFMAs touches them.
+    float by = 1.0f;
+    auto do_step = [&](int step) -> bool {
+      // the step's keys are in their slot, and every wave has left the slot
+      // that the next issue fills
+      if (S::kDistance == 2 && step + 1 < step_end)
+        wait_and_barrier<S::kOctets * kOctLoads>();
+      else
+        wait_and_barrier<0>();
+      if (step + S::kDistance < step_end) issue(step + S::kDistance);
+      const int slot = (step - step0) & (S::kSlots - 1);
+      const uint32_t base = ring + slot * S::kSlotBytes + (S::kWide ? 0 : ts * ST * kBlkBytes);
 
       // ---- S = K Q^T
-      f32x4 s[PT][ST];
+      float z[kScores];
+      if constexpr (S::kWide) {
+        f32x16 s0 = {}, s1 = {};  // two chains
+        constexpr int kRing = 8;  // operands: 6 read ahead
+        s16x8 kk[kRing];
+        auto read = [&](int ks) { kk[ks % kRing] = lds_read(base + (k_at ^ ((ks & 3) * 32)) + (ks >> 2) * 1024); };
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
+        for (int ks = 0; ks < kRing - 2; ++ks) read(ks);
 #pragma unroll
-        for (int st = 0; st < ST; ++st) s[pt][st] = f32x4{0, 0, 0, 0};
+        for (int ks = 0; ks < kQ; ks += 2) {
 #pragma unroll
-      for (int ks = 0; ks < kKSteps; ++ks) {
+          for (int i = 0; i < 2; ++i)
+            if (ks + kRing - 2 + i < kQ) read(ks + kRing - 2 + i);
+          __builtin_amdgcn_sched_barrier(0);
+          s0 = E::mfma_wide(kk[ks % kRing], q[ks], s0);
+          s1 = E::mfma_wide(kk[(ks + 1) % kRing], q[ks + 1], s1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          const s16x8 kk = lds_read((blk0 + (ks & 1 ? k_at ^ 64 : k_at)) + st * kBlkBytes + (ks >> 1) * 1024);
+        for (int i = 0; i < kScores; ++i) z[i] = s0[i] + s1[i];
+      } else {
+        constexpr int kChains = ST == 1 ? 2 : 1;
+        constexpr int kReads = kKSteps * ST, kRing = 8;
+        f32x4 s[ST][kChains] = {};
+        s16x8 kk[kRing];
+        auto read = [&](int r) {
+          const int ks = r / ST, st = r % ST;
+          kk[r % kRing] = lds_read(base + (k_at ^ ((ks & 1) * 64)) + st * kBlkBytes + (ks >> 1) * 1024);
+        };
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt) s[pt][st] = E::mfma32(kk, q[pt][ks], s[pt][st]);
+        for (int r = 0; r < kRing - 2; ++r) read(r);
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) {
+          if (r % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (r + kRing - 2 + i < kReads) read(r + kRing - 2 + i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          const int ks = r / ST, st = r % ST;
+          s[st][ks % kChains] = E::mfma32(kk[r % kRing], q[ks], s[st][ks % kChains]);
+          if (r % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < kScores; ++i) {
+          z[i] = s[i / 4][0][i % 4];
+          if constexpr (kChains == 2) z[i] += s[i / 4][1][i % 4];
         }
       }
 
-      // ---- scores in powers of two, masked keys at -inf
-      const int key0 = (it.tile0 + t) * kTile + ts * ST * 16 + 4 * g4;  // dense: + 16 st + i
-      int tok[ST][4];
+      // ---- scores in powers of two, masked keys at -inf.  Score i is key
+      // key_of(i) of the wave's part of the step.
+      auto key_of = [&](int i) {
+        return S::kWide ? 8 * (i >> 2) + 4 * half + (i & 3) : ts * ST * 16 + 16 * (i >> 2) + 4 * g4 + (i & 3);
+      };
+      const int step_key = step * S::kKeys;  // of the item's list
+      if (a.softcap > 0.0f) {
+        const float by = a.scale / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
-      for (int st = 0; st < ST; ++st)
+        for (int i = 0; i < kScores; ++i) z[i] = cap * tanh_f32(z[i] * by);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          tok[st][i] = KIND == kSparse ? s_tok[slot][(ts * ST + st) * 16 + 4 * g4 + i] : key0 + st * 16 + i;
-      const int tile_lo = (it.tile0 + t) * kTile;
-      const bool masked = KIND == kSparse || tile_lo < it.max_start || tile_lo + kTile > it.min_end;
-      // some key that is read is hidden from some row
-      const bool mixed = KIND != kSparse && (max(tile_lo, it.min_start) < it.max_start ||
-                                             min(tile_lo + kTile, it.max_end) > it.min_end);
+        for (int i = 0; i < kScores; ++i) z[i] *= to_log2;
+      }
+      if (a.slopes) {
+        const int32_t* list = KIND == kSparse ? a.indices + static_cast<int64_t>(it.row0) * a.k : nullptr;
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          if (a.softcap > 0.0f) {
-            const float by = a.scale / a.softcap, cap = a.softcap * kLog2e;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[pt][st][i] = cap * tanh_f32(s[pt][st][i] * by);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[pt][st][i] *= to_log2;
-          }
-          if (a.slopes) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[pt][st][i] -= p_slope[pt] * fabsf(static_cast<float>(p_pos[pt] - tok[st][i]));
-          }
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool seen = KIND == kSparse ? tok[st][i] >= 0 : tok[st][i] >= p_start[pt] && tok[st][i] < p_end[pt];
-              s[pt][st][i] = seen ? s[pt][st][i] : -__builtin_inff();
-            }
-          }
-        }
-
-      // ---- running maximum and sum
-      s16x4 p[PT][ST];
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-        float mx = s[pt][0][0];
-#pragma unroll
-        for (int st = 0; st < ST; ++st)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[pt][st][i]);
-        mx = pair_max(mx) - E::kShift;
-        if (__ballot(mx > m[pt] + kRaise)) {
-          const float raised = fmaxf(m[pt], mx);
-          const float by = __builtin_amdgcn_exp2f(m[pt] - raised);
-          m[pt] = raised;
-          l[pt] *= by;
-#pragma unroll
-          for (int d = 0; d < kDimTiles; ++d) acc[pt][d] *= by;
-        }
-#pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          float e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f(s[pt][st][i] - m[pt]);
-          l[pt] += (e[0] + e[1]) + (e[2] + e[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[pt][st][i] = E::round(e[i]);
+        for (int i = 0; i < kScores; ++i) {
+          const int c = step_key + key_of(i);
+          const int tok = KIND == kSparse ? list[min(c, a.k - 1)] : it.tile0 * kTile + c;
+          z[i] -= p_slope * fabsf(static_cast<float>(p_pos - tok));
         }
       }
+      bool mixed = false;  // some key that was read is hidden from some row
+      if constexpr (KIND == kSparse) {
+        uint32_t live[2];
+        if constexpr (S::kWide) {
+          live[0] = s_live[slot][0] | s_live[slot][1] << 8 | s_live[slot][2] << 16 | s_live[slot][3] << 24;
+          live[1] = ~0u;
+        } else {
+          live[0] = s_live[slot][0] | s_live[slot][1] << 16;
+          live[1] = s_live[slot][2] | s_live[slot][3] << 16;
+        }
+        if (__builtin_amdgcn_readfirstlane(live[0] & live[1]) != -1) {
+#pragma unroll
+          for (int i = 0; i < kScores; ++i) {
+            const int c = key_of(i);
+            const uint32_t word = S::kWide || c < 32 ? live[0] : live[1];
+            z[i] = (word >> (c & 31)) & 1 ? z[i] : -__builtin_inff();
+          }
+        }
+      } else {
+        const int first = it.tile0 * kTile + step_key;
+        mixed = max(first, it.min_start) < it.max_start || min(first + S::kKeys, it.max_end) > it.min_end;
+        if (first < it.max_start || first + S::kKeys > it.min_end) {
+#pragma unroll
+          for (int i = 0; i < kScores; ++i) {
+            const int tok = first + key_of(i);
+            z[i] = tok >= p_start && tok < p_end ? z[i] : -__builtin_inff();
+          }
+        }
+      }
+
+      // ---- running maximum: raised where a score passes it by kRaise
+      float mx = z[0];
+#pragma unroll
+      for (int i = 1; i < kScores; ++i) mx = fmaxf(mx, z[i]);
+      mx = pair_max<S::kWide>(mx) - E::kShift;
+      const float raised = mx > m + E::kRaise ? mx : m;
+      const bool any_raised = step > step0 && __ballot(raised != m) != 0;  // nothing to rescale in the first step
+      by = __builtin_amdgcn_exp2f(m - raised);
+      m = raised;
 
       // A key that some rows of the pair tile see and others do not may hold an
       // infinity or a NaN; a weight of zero would not take it out of the
       // product.  Rows that see it get their NaN from S.
-      if constexpr (KIND != kSparse) {
-        if (mixed) {
-          __syncthreads();
-          for (int i = tid; i < kSlotBytes / 16; i += kAttnThreads) {
-            s16x8* v = reinterpret_cast<s16x8*>(s_keys + slot * kSlotBytes) + i;
-            s16x8 x = *v;
-            constexpr int kExp = DT == IDX_BF16 ? 0x7F80 : 0x7C00;
+      auto clear_nonfinite = [&] {
+        __syncthreads();
+        for (int i = tid; i < S::kSlotBytes / 16; i += kAttnThreads) {
+          s16x8* v = reinterpret_cast<s16x8*>(s_keys + slot * S::kSlotBytes) + i;
+          s16x8 x = *v;
+          constexpr int kExp = DT == IDX_BF16 ? 0x7F80 : 0x7C00;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (x[j] & kExp) == kExp ? 0 : x[j];
-            *v = x;
-          }
-          __syncthreads();
+          for (int j = 0; j < 8; ++j) x[j] = (x[j] & kExp) == kExp ? 0 : x[j];
+          *v = x;
         }
+        __syncthreads();
+      };
+      if constexpr (KIND != kSparse) {
+        if (mixed) clear_nonfinite();
       }
 
-      // ---- O^T += V^T P^T
+      if constexpr (S::kWide) {
+        // ---- the step before: O^T += V^T P^T, with this step's exponentials
+        // between its MFMAs; then the accumulators take the new maximum
+        // (the first step has none before it: weights of zero on its own keys,
+        // which every row of the pair tile sees or whose non-finite values
+        // have just been cleared)
+        s16x8 p_next[2];
+        float sum = 0.0f;
+        value_wide(step > step0 ? ring + ((step - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes : base, [&](int i) {
+          const float e = __builtin_amdgcn_exp2f(z[i] - m);
+          sum += e;
+          p_next[i / 8][i % 8] = E::round(e);
+        });
+        p_wide[0] = p_next[0];
+        p_wide[1] = p_next[1];
+        l = l * by + sum;
+        return any_raised;
+      } else {
+        if (any_raised) {
+          l *= by;
 #pragma unroll
-      for (int d = 0; d < kDimTiles; ++d) {
-        const uint32_t va = blk0 + (v_at ^ ((d & 3) * 32)) + (d >> 2) * 1024;
-        if constexpr (ST == 1) {
-          const s16x4 v = lds_read_tr(va);
+          for (int d = 0; d < kAccs; ++d) acc[d] *= by;
+        }
+        s16x4 p[ST];
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][d] = E::mfma16(v, p[pt][0], acc[pt][d]);
-        } else {
+        for (int st = 0; st < ST; ++st) {
+          float e[4];
 #pragma unroll
-          for (int st = 0; st < ST; st += 2) {
-            const s16x4 v0 = lds_read_tr(va + st * kBlkBytes), v1 = lds_read_tr(va + (st + 1) * kBlkBytes);
-            const s16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+          for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f(z[st * 4 + i] - m);
+          l += (e[0] + e[1]) + (e[2] + e[3]);
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-              const s16x8 pp = __builtin_shufflevector(p[pt][st], p[pt][st + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-              acc[pt][d] = E::mfma32(v, pp, acc[pt][d]);
+          for (int i = 0; i < 4; ++i) p[st][i] = E::round(e[i]);
+        }
+        // ---- O^T += V^T P^T
+        if constexpr (!S::kWide) {
+          constexpr int kRing = ST == 1 ? 10 : ST == 2 ? 6 : 4;
+          s16x4 v[kRing][ST];
+          auto read = [&](int d) {
+#pragma unroll
+            for (int st = 0; st < ST; ++st)
+              v[d % kRing][st] = lds_read_tr(base + (v_at ^ ((d & 3) * 32)) + (d >> 2) * 1024 + st * kBlkBytes);
+          };
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int d = 0; d < kRing - 2; ++d) read(d);
+#pragma unroll
+          for (int d = 0; d < kAccs; ++d) {
+            if (d % 2 == 0) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (d + kRing - 2 + i < kAccs) read(d + kRing - 2 + i);
+              __builtin_amdgcn_sched_barrier(0);
             }
+            if constexpr (ST == 1) {
+              acc[d] = E::mfma16(v[d % kRing][0], p[0], acc[d]);
+            } else {
+#pragma unroll
+              for (int st = 0; st < ST; st += 2)
+                acc[d] = E::mfma32(__builtin_shufflevector(v[d % kRing][st], v[d % kRing][st + 1], 0, 1, 2, 3, 4, 5, 6, 7),
+                                   __builtin_shufflevector(p[st], p[st + 1], 0, 1, 2, 3, 4, 5, 6, 7), acc[d]);
+            }
+            if (d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
           }
         }
+        return false;
       }
+    };
+    if constexpr (S::kWide) {
+      for (int step = step0; step < step_end;) {
+#pragma unroll
+        for (int d = 0; d < kAccs; ++d) pin(acc[d]);
+        bool raise;
+        do {
+          raise = do_step(step);
+          ++step;
+        } while (!raise && step < step_end);
+        if (raise) {
+#pragma unroll
+          for (int d = 0; d < kAccs; ++d) {  // one at a time: there are registers for one
+            settle(acc[d]);
+            acc[d] *= by;
+            pin(acc[d]);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < kAccs; ++d) pin(acc[d]);
+      }
+#pragma unroll
+      for (int d = 0; d < kAccs; ++d) pin(acc[d]);
+      value_wide(ring + ((step_end - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes, [](int) {});
+    } else {
+      for (int step = step0; step < step_end; ++step) do_step(step);
     }
 
     // ---- the streams' parts of each pair become one, 128 dimensions at a
     // time through LDS, and leave as whole rows
-#pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
-      const float sum = pair_sum(l[pt]);
-      if (g4 == 0) s_ml[wave][pt * 16 + n16] = make_float2(m[pt], sum);
+    {
+      const float sum = pair_sum<S::kWide>(l);
+      if (lane < S::kWavePairs) s_ml[wave][lane] = make_float2(m, sum);
     }
-    __syncthreads();  // every wave has left the last tile, and s_ml is complete
-    const int64_t pair_base = static_cast<int64_t>(it.row0) * a.heads + it.pair0;  // over the whole batch
+    lds_barrier();  // every wave has left the last step, and s_ml is complete
     float* piece = nullptr;
     if (!whole) {
       const int64_t id = KIND == kShared ? static_cast<int64_t>(w) + item : (lo == 0 ? 2 * w + 1 : 2 * w);
       piece = pieces + id * piece_floats(M);
     }
+    // 64 (narrow) or 128 (wide) rows of accumulators; the pad of 4 floats
+    // spreads the pairs over all banks
+    constexpr int kChunks = S::kWide ? 2 : 1, kChunkDims = kValDim / kChunks, kStride = kChunkDims + 4;
     float* s_o = reinterpret_cast<float*>(s_keys);
-    for (int c = 0; c < kValDim / kChunkDims; ++c) {
-      if (c) __syncthreads();
+    float* mine = s_o + (wave * S::kWavePairs + col) * kStride;
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
+    for (int c = 0; c < kChunks; ++c) {
+      if (c) lds_barrier();  // stores to memory go on meanwhile
+      if constexpr (S::kWide) {
 #pragma unroll
-        for (int d = 0; d < kDimTiles; ++d)
-          if (d / 8 == c)
-            *reinterpret_cast<f32x4*>(s_o + (wave * kWavePairs + pt * 16 + n16) * kChunkStride + (d % 8) * 16 +
-                                      4 * g4) = acc[pt][d];
-      __syncthreads();
-      for (int i = tid; i < M * (kChunkDims / 4); i += kAttnThreads) {
+        for (int d = 8 * c; d < 8 * c + 8; ++d) {
+          settle(acc[d]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4*>(mine + (d & 7) * 32 + 8 * i + 4 * half) =
+                f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < kAccs; ++d) {
+          if constexpr (!S::kWide) *reinterpret_cast<f32x4*>(mine + d * 16 + 4 * g4) = acc[d];
+        }
+      }
+      lds_barrier();
+#pragma unroll 2
+      for (int i = tid; i < it.pairs * (kChunkDims / 4); i += kAttnThreads) {
         const int local = i / (kChunkDims / 4), dim = (i % (kChunkDims / 4)) * 4;
-        const int group = local / kWavePairs, in = local % kWavePairs;
-        if (local >= it.pairs) continue;
+        const int group = local / S::kWavePairs, in = local % S::kWavePairs;
         float top = kMInit;
 #pragma unroll
-        for (int k = 0; k < TS; ++k) top = fmaxf(top, s_ml[group * TS + k][in].x);
+        for (int k = 0; k < S::kStreams; ++k) top = fmaxf(top, s_ml[group * S::kStreams + k][in].x);
         f32x4 o = {0, 0, 0, 0};
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < TS; ++k) {
-          const float2 ml = s_ml[group * TS + k][in];
-          const float by = TS == 1 ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
-          sum += ml.y * by;
-          o += *reinterpret_cast<const f32x4*>(s_o + ((group * TS + k) * kWavePairs + in) * kChunkStride + dim) * by;
+        for (int k = 0; k < S::kStreams; ++k) {
+          const int from = group * S::kStreams + k;
+          const float2 ml = s_ml[from][in];
+          const float part = S::kStreams == 1 ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
+          sum += ml.y * part;
+          o += *reinterpret_cast<const f32x4*>(s_o + (from * S::kWavePairs + in) * kStride + dim) * part;
         }
         if (whole) {
           const int64_t pair = pair_base + local;
@@ -786,7 +1046,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       }
     }
     if (!whole && lo == 0 && tid == 0) {
-      const int last = share_owner(share.total, share.groups, item_at + it.tiles - 1);
+      const int last = share_owner(share.total, share.groups, tiles_at + it.tiles - 1);
       JoinInfo j;
       j.pair0 = pair_base;
       j.pairs = it.pairs;
@@ -796,9 +1056,6 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       j.pad2 = 0;
       join[KIND == kShared ? item : w] = j;
     }
-    at = item_at + hi;
-    item_at += it.tiles;
-    ++item;
   }
 }
 
@@ -815,20 +1072,34 @@ struct Joined {
   float m, l;
 };
 
+// Adds n pieces: 64 at a time, first their maxima and sums (one lane each),
+// then their rows, whose loads do not wait for one another.
 template <class At>
 __device__ __forceinline__ void join_list(Joined& j, int n, int M, int local, At at) {
   const int lane = lane_id();
-  for (int i = 0; i < n; ++i) {
-    const float* piece = at(i);
-    const float2 ml = reinterpret_cast<const float2*>(piece + M * kValDim)[local];
-    const f32x4* o = reinterpret_cast<const f32x4*>(piece + static_cast<int64_t>(local) * kValDim + lane * 8);
-    const f32x4 a = o[0], b = o[1];
-    const float top = fmaxf(j.m, ml.x);
-    const float mine = __builtin_amdgcn_exp2f(j.m - top), theirs = __builtin_amdgcn_exp2f(ml.x - top);
-    j.o0 = j.o0 * mine + a * theirs;
-    j.o1 = j.o1 * mine + b * theirs;
-    j.l = j.l * mine + ml.y * theirs;
+  for (int i0 = 0; i0 < n; i0 += kWave) {
+    float2 ml = make_float2(kMInit, 0.0f);
+    if (i0 + lane < n) ml = reinterpret_cast<const float2*>(at(i0 + lane) + M * kValDim)[local];
+    float top = ml.x;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    top = fmaxf(top, j.m);
+    const float mine = __builtin_amdgcn_exp2f(j.m - top), part = __builtin_amdgcn_exp2f(ml.x - top);
+    float sum = ml.y * part;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) sum += __shfl_xor(sum, d);
+    j.l = j.l * mine + sum;
     j.m = top;
+    j.o0 *= mine;
+    j.o1 *= mine;
+    const int some = min(n - i0, kWave);
+#pragma unroll 8
+    for (int i = 0; i < some; ++i) {
+      const f32x4* o = reinterpret_cast<const f32x4*>(at(i0 + i) + static_cast<int64_t>(local) * kValDim + lane * 8);
+      const float by = __shfl(part, i);
+      j.o0 += o[0] * by;
+      j.o1 += o[1] * by;
+    }
   }
 }
 
@@ -882,29 +1153,27 @@ __global__ __launch_bounds__(256) void join_shared_kernel(JoinArgs a, int M, int
 }
 
 // Pairs of a pair tile, by the pairs that one request brings (its rows' heads):
-// as few idle matrix columns as possible, and beyond 64 the same keys are read
-// again by the next tile.
+// as few idle matrix columns as possible.
 int tile_pairs(int64_t pairs_per_request) {
-  return pairs_per_request <= 16 ? 16 : pairs_per_request <= 32 ? 32 : 64;
+  return pairs_per_request <= 16 ? 16 : pairs_per_request <= 32 ? 32 : pairs_per_request <= 64 ? 64 : 128;
 }
 
 constexpr int kMaxGrid = 256;  // one persistent workgroup per CU
-constexpr int kMinTiles = 2;   // smallest share: below, the join costs more than the split saves
+constexpr int kMinUnits = kItemCost + 2;  // smallest share: below, the join costs more than the split saves
 
 size_t join_bytes(int64_t infos) { return (static_cast<size_t>(infos) * sizeof(JoinInfo) + 255) / 256 * 256; }
 
-template <int DT, int KIND, int PT, int PG>
+template <int DT, int KIND, int M>
 hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
-  constexpr int M = 16 * PT * PG;
   const int64_t items = item_count<KIND, M>(a);
   const int64_t tiles = KIND == kSparse ? (a.k + kTile - 1) / kTile : a.max_pages;
-  const int grid = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * tiles / kMinTiles)));
+  const int grid = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + kItemCost) / kMinUnits)));
   JoinInfo* info = static_cast<JoinInfo*>(a.workspace);
   float* pieces = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
                                            join_bytes(KIND == kShared ? items : kMaxGrid));
   const bool joins = KIND == kShared || grid > 1;
-  launch_kernel(attention_kernel<DT, KIND, PT, PG>, dim3(grid), dim3(kAttnThreads), stream, ev.start,
-                joins ? nullptr : ev.stop, a, kMinTiles, info, pieces);
+  launch_kernel(attention_kernel<DT, KIND, M>, dim3(grid), dim3(kAttnThreads), stream, ev.start,
+                joins ? nullptr : ev.stop, a, kMinUnits, info, pieces);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !joins) return e;
   const JoinArgs j{info, pieces, a.out, a.lse};
@@ -923,9 +1192,10 @@ hipError_t launch_kind(const AttentionArgs& a, hipStream_t stream, LaunchEvents 
   const int64_t per_request = KIND == kSparse ? a.heads
                                               : (static_cast<int64_t>(a.rows) + a.requests - 1) / a.requests * a.heads;
   switch (tile_pairs(per_request)) {
-    case 16: return launch<DT, KIND, 1, 1>(a, stream, ev);
-    case 32: return launch<DT, KIND, 1, 2>(a, stream, ev);
-    default: return launch<DT, KIND, 1, 4>(a, stream, ev);
+    case 16: return launch<DT, KIND, 16>(a, stream, ev);
+    case 32: return launch<DT, KIND, 32>(a, stream, ev);
+    case 64: return launch<DT, KIND, 64>(a, stream, ev);
+    default: return launch<DT, KIND, 128>(a, stream, ev);
   }
 }
 
