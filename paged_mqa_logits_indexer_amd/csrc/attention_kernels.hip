@@ -49,6 +49,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -79,14 +82,19 @@ struct Elem<IDX_BF16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
   }
-  static __device__ __forceinline__ void mfma_acc(s16x8 a, s16x8 b, f32x16& c) {
-    __asm__ volatile("s_nop 1\nv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  static __device__ __forceinline__ void mfma_acc(s16x8 a0, s16x8 a1, s16x8 b, f32x16& c0, f32x16& c1) {
+    __asm__ volatile("s_nop 1\nv_mfma_f32_32x32x16_bf16 %0, %2, %4, %0\nv_mfma_f32_32x32x16_bf16 %1, %3, %4, %1"
+                     : "+a"(c0), "+a"(c1)
+                     : "v"(a0), "v"(a1), "v"(b));
   }
   static __device__ __forceinline__ f32x4 mfma16(s16x4 a, s16x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ short round(float x) {
     return __builtin_bit_cast(short, static_cast<__bf16>(x));
+  }
+  static __device__ __forceinline__ int round2(float x, float y) {
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{x, y}), bf16x2));
   }
 };
 template <>
@@ -100,8 +108,10 @@ struct Elem<IDX_FP16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
   }
-  static __device__ __forceinline__ void mfma_acc(s16x8 a, s16x8 b, f32x16& c) {
-    __asm__ volatile("s_nop 1\nv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  static __device__ __forceinline__ void mfma_acc(s16x8 a0, s16x8 a1, s16x8 b, f32x16& c0, f32x16& c1) {
+    __asm__ volatile("s_nop 1\nv_mfma_f32_32x32x16_f16 %0, %2, %4, %0\nv_mfma_f32_32x32x16_f16 %1, %3, %4, %1"
+                     : "+a"(c0), "+a"(c1)
+                     : "v"(a0), "v"(a1), "v"(b));
   }
   static __device__ __forceinline__ f32x4 mfma16(s16x4 a, s16x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
@@ -109,6 +119,9 @@ struct Elem<IDX_FP16> {
   }
   static __device__ __forceinline__ short round(float x) {
     return __builtin_bit_cast(short, static_cast<_Float16>(x));
+  }
+  static __device__ __forceinline__ int round2(float x, float y) {
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{x, y}), f16x2));
   }
 };
 
@@ -150,19 +163,26 @@ __device__ __forceinline__ int key_offset(int key) { return (key >> 3) * kOctByt
 // the other slots; the caller waits (vmcnt) before the barrier that publishes
 // the keys.
 constexpr int kOctLoads = 9;
-__device__ __forceinline__ void load_octet(const char* at, uint32_t lds) {
-#define PMQA_LOAD(j, m)             \
-  "s_add_u32 m0, %[l], " m "\n"     \
-  "s_nop 0\n"                       \
-  "global_load_lds_dwordx4 %[a], off offset:" j "\n"
+template <int J>
+__device__ __forceinline__ void load_piece(const char* at, uint32_t lds) {
   __asm__ volatile(
-      PMQA_LOAD("0", "0") PMQA_LOAD("128", "896") PMQA_LOAD("256", "1792") PMQA_LOAD("384", "2688")
-      PMQA_LOAD("512", "3584") PMQA_LOAD("640", "4480") PMQA_LOAD("768", "5376") PMQA_LOAD("896", "6272")
-      PMQA_LOAD("1024", "7168")
+      "s_add_u32 m0, %0, %2\n"
+      "s_nop 0\n"
+      "global_load_lds_dwordx4 %1, off offset:%3"
       :
-      : [l] "s"(lds), [a] "v"(at)
+      : "s"(lds), "v"(at), "n"(J * 896), "n"(J * 128)
       : "memory", "m0", "scc");
-#undef PMQA_LOAD
+}
+__device__ __forceinline__ void load_octet(const char* at, uint32_t lds) {
+  load_piece<0>(at, lds);
+  load_piece<1>(at, lds);
+  load_piece<2>(at, lds);
+  load_piece<3>(at, lds);
+  load_piece<4>(at, lds);
+  load_piece<5>(at, lds);
+  load_piece<6>(at, lds);
+  load_piece<7>(at, lds);
+  load_piece<8>(at, lds);
 }
 
 // Waits until at most LEFT vector memory operations of this wave are
@@ -175,6 +195,13 @@ __device__ __forceinline__ void wait_and_barrier() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | ((LEFT >> 4) << 14));
   __builtin_amdgcn_s_barrier();
   __asm__ volatile("" ::: "memory");
+}
+
+// A value whose origin the compiler does not see: constants added to such an
+// LDS address become the read's own offset instead of an addition per read.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  __asm__("" : "+v"(x));
+  return x;
 }
 
 typedef __attribute__((address_space(3))) const s16x8* LdsVec8;
@@ -510,6 +537,14 @@ struct Shape {
   static constexpr int kBlocks = kWide ? 2 : kKeys / 16 / kStreams;  // 16-key blocks of a step per wave
 };
 
+// What masks and the bias need to know of a pair; read when they do (the wide
+// form has no registers to keep it in).
+struct alignas(16) PairInfo {
+  int start, end;  // keys that its row sees
+  int pos;
+  float slope;     // in powers of two
+};
+
 template <int DT, int KIND, int M>
 __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArgs a, int min_units, JoinInfo* join,
                                                                     float* pieces) {
@@ -521,6 +556,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   __shared__ int s_rows[KIND == kSparse ? kWindow : 1];       // sparse: cache row of each listed key, -1: none
   __shared__ uint32_t s_live[S::kSlots][4];                   // sparse: bits of the keys that are there
   __shared__ float2 s_ml[4][S::kWavePairs];
+  __shared__ PairInfo s_pair[S::kWavePairs * S::kGroups];
   __shared__ int64_t s_res[2];
   __shared__ int s_scan[KIND == kSparse ? 8 + 640 : kAttnThreads / kWave + kScanChunks];
 
@@ -552,6 +588,10 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   const int capacity = a.max_pages * kPage;
   const char* cache = static_cast<const char*>(a.cache);
   const float to_log2 = a.scale * kLog2e;
+  // wide: the factor is applied with the exponential's subtraction, unless the
+  // score is changed in between (or the factor turns the order round)
+  const bool prescale = a.softcap > 0.0f || a.slopes || !(to_log2 > 0.0f);
+  const float z_scale = prescale ? 1.0f : to_log2;
 
   const int items = static_cast<int>(item_count<KIND, M>(a));
   int64_t at = share.t0;
@@ -572,44 +612,53 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     // ---- loading
     int page_window = -1, window_page = 0;  // dense: page ids of 64 tiles, one per lane
     int row_window = -1;                    // sparse: window of keys in s_rows
-    // sparse: cache rows of kWindow listed keys, two dependent loads for all of them at once
-    auto resolve = [&](int window) {
+    // sparse: cache rows of kWindow listed keys, two dependent loads for AT of
+    // them per thread at a time (all at the beginning, one by one where a list
+    // longer than the window goes on between two steps: there the loop's
+    // registers have no room for more)
+    auto resolve = [&](int window, auto many) {
+      constexpr int AT = decltype(many)::value;
       row_window = window;
       const int32_t* list = a.indices + static_cast<int64_t>(it.row0) * a.k + window * kWindow;
       const int n = min(kWindow, a.k - window * kWindow);
-      int tok[kWindow / kAttnThreads];
+#pragma unroll 1
+      for (int i0 = tid; i0 < kWindow; i0 += AT * kAttnThreads) {
+        int tok[AT], page[AT];
 #pragma unroll
-      for (int i = 0; i < kWindow / kAttnThreads; ++i) {
-        const int c = i * kAttnThreads + tid;
-        tok[i] = c < n ? list[c] : -1;
+        for (int i = 0; i < AT; ++i) tok[i] = i0 + i * kAttnThreads < n ? list[i0 + i * kAttnThreads] : -1;
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+          if (tok[i] >= capacity) tok[i] = -1;
+          page[i] = tok[i] >= 0 ? table[tok[i] / kPage] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < AT; ++i)
+          s_rows[i0 + i * kAttnThreads] =
+              tok[i] >= 0 ? max(0, min(page[i], a.num_pages - 1)) * kPage + (tok[i] & (kPage - 1)) : -1;
       }
-      int page[kWindow / kAttnThreads];
-#pragma unroll
-      for (int i = 0; i < kWindow / kAttnThreads; ++i) {
-        if (tok[i] >= capacity) tok[i] = -1;
-        page[i] = tok[i] >= 0 ? table[tok[i] / kPage] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < kWindow / kAttnThreads; ++i)
-        s_rows[i * kAttnThreads + tid] =
-            tok[i] >= 0 ? max(0, min(page[i], a.num_pages - 1)) * kPage + (tok[i] & (kPage - 1)) : -1;
     };
     const char* zero = reinterpret_cast<const char*>(kZeroRow);
-    auto issue = [&](int step) {
+    const char* from[S::kOctets];  // next loads: this lane's source ...
+    uint32_t to[S::kOctets];       // ... and the wave's place in the ring
+    // (the wide form also loads the two steps after the last, from the row of
+    // zeros: it then has no branch between its MFMAs)
+    auto locate = [&](int step) {
       const int slot = (step - step0) & (S::kSlots - 1);
+      const bool any = step < step_end;
       int page = 0;
       const int key0 = step * S::kKeys + wave * (8 * S::kOctets);  // this wave's first key of the item's list
       if constexpr (KIND == kSparse) {
-        if (key0 / kWindow != row_window) {  // the same for all waves: a window is whole steps
+        if (any && key0 / kWindow != row_window) {  // the same for all waves: a window is whole steps
           lds_barrier();
-          resolve(key0 / kWindow);
+          resolve(key0 / kWindow, std::integral_constant<int, 1>{});
           lds_barrier();
         }
       } else {
-        const int tile = it.tile0 + key0 / kTile;
+        const int tile = it.tile0 + min(key0 / kTile, it.tiles - 1);
         if ((tile >> 6) != page_window) {
           page_window = tile >> 6;
           window_page = table[min(page_window * 64 + lane, a.max_pages - 1)];
+          __asm__ volatile("" : "+v"(window_page));  // waited for here, not in the steps that only read it
         }
         page = max(0, min(__builtin_amdgcn_readlane(window_page, tile & 63), a.num_pages - 1));
       }
@@ -621,7 +670,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         bool live;
         if constexpr (KIND == kSparse) {
           row = s_rows[key & (kWindow - 1)];
-          live = row >= 0;
+          live = any && row >= 0;
           const uint64_t mask = __ballot(live);
 #pragma unroll
           for (int i = 0; i < 8; ++i) live_bits |= static_cast<uint32_t>(mask >> (8 * i) & 1) << (8 * o + i);
@@ -629,13 +678,31 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
           // keys that no row of the pair tile sees are not read
           const int tok = it.tile0 * kTile + key;
           row = page * kPage + (key & (kPage - 1));
-          live = tok >= it.min_start && tok < it.max_end;
+          live = any && tok >= it.min_start && tok < it.max_end;
         }
-        const char* from = (live ? cache + static_cast<int64_t>(row) * kRowBytes : zero) +
-                           (((lane & 7) ^ swz((8 * ((wave * S::kOctets + o) & 1)) + (lane >> 3))) * 16);
-        load_octet(from, ring + slot * S::kSlotBytes + (wave * S::kOctets + o) * kOctBytes);
+        from[o] = (live ? cache + static_cast<int64_t>(row) * kRowBytes : zero) +
+                  (((lane & 7) ^ swz((8 * ((wave * S::kOctets + o) & 1)) + (lane >> 3))) * 16);
+        to[o] = ring + slot * S::kSlotBytes + (wave * S::kOctets + o) * kOctBytes;
       }
       if (KIND == kSparse && lane == 0) s_live[slot][wave] = live_bits;
+    };
+    auto load_one = [&](int j) {  // wide: j is a constant of the unrolled loop
+      switch (j) {
+        case 0: return load_piece<0>(from[0], to[0]);
+        case 1: return load_piece<1>(from[0], to[0]);
+        case 2: return load_piece<2>(from[0], to[0]);
+        case 3: return load_piece<3>(from[0], to[0]);
+        case 4: return load_piece<4>(from[0], to[0]);
+        case 5: return load_piece<5>(from[0], to[0]);
+        case 6: return load_piece<6>(from[0], to[0]);
+        case 7: return load_piece<7>(from[0], to[0]);
+        case 8: return load_piece<8>(from[0], to[0]);
+      }
+    };
+    auto issue = [&](int step) {
+      locate(step);
+#pragma unroll
+      for (int o = 0; o < S::kOctets; ++o) load_octet(from[o], to[o]);
     };
 
     // ---- the queries come through the ring as well (whole 128-byte pieces; the
@@ -651,22 +718,24 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
                          (((lane & 7) ^ swz(pair & 15)) * 16);
       load_octet(from, q_ring + o * kOctBytes);
     }
-    int p_start = 0, p_end = capacity, p_pos;
-    float p_slope;
-    {
-      const int pair = it.pair0 + min(pg * S::kWavePairs + col, it.pairs - 1);
+    for (int local = tid; local < M; local += kAttnThreads) {
+      const int pair = it.pair0 + min(local, it.pairs - 1);
       const int row = it.row0 + pair / a.heads;
+      PairInfo info{0, capacity, 0, 0.0f};
       if constexpr (KIND != kSparse) {
-        p_end = clamp_len(a.row_lens[row], capacity);
-        if (a.row_starts) p_start = max(0, a.row_starts[row]);
+        info.end = clamp_len(a.row_lens[row], capacity);
+        if (a.row_starts) info.start = max(0, a.row_starts[row]);
       }
-      p_slope = a.slopes ? a.slopes[pair % a.heads] * kLog2e : 0.0f;
-      p_pos = a.row_positions ? a.row_positions[row] : p_end - 1;
-      p_start = max(p_start, it.key_lo);
-      p_end = min(p_end, it.key_hi);
+      if (a.slopes) {
+        info.slope = a.slopes[pair % a.heads] * kLog2e;
+        info.pos = a.row_positions ? a.row_positions[row] : info.end - 1;
+      }
+      info.start = max(info.start, it.key_lo);
+      info.end = min(info.end, it.key_hi);
+      s_pair[local] = info;
     }
     if constexpr (KIND == kSparse) {
-      resolve(step0 * S::kKeys / kWindow);
+      resolve(step0 * S::kKeys / kWindow, std::integral_constant<int, kWindow / kAttnThreads>{});
       lds_barrier();
     }
     // narrow: slot 0 holds step0's keys, slot 1 the queries
@@ -683,8 +752,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     lds_barrier();
     if constexpr (S::kWide) {
 #pragma unroll
-      for (int d = 0; d < S::kDistance; ++d)
-        if (step0 + d < step_end) issue(step0 + d);
+      for (int d = 0; d < S::kDistance; ++d) issue(step0 + d);
     }
 
     // accumulators: dimensions on the rows, pairs on the columns
@@ -695,39 +763,55 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
 #pragma unroll
     for (int d = 0; d < kAccs; ++d) acc[d] = Acc{};
     float m = kMInit, l = 0.0f;
-    s16x8 p_wide[2] = {};  // wide: weights of the step before
+    // wide: scores of the step before (of none before the first: weights of zero)
+    // and its weights
+    float z_before[kScores];
+    i32x4 p_wide[2];
+#pragma unroll
+    for (int i = 0; i < kScores; ++i) z_before[i] = -__builtin_inff();
+    auto weigh = [&](int i, float& sum) {  // scores 2 i and 2 i + 1
+      const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(z_before[2 * i], z_scale, -m));
+      const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(z_before[2 * i + 1], z_scale, -m));
+      sum += e0 + e1;
+      int both = E::round2(e0, e1);
+      __asm__ volatile("" : "+v"(both), "+v"(sum));  // computed here, between the MFMAs, and not where it is used
+      p_wide[i / 4][i % 4] = both;
+    };
 
     // the value product of one step (wide), V^T P^T on the keys at `base`; each
     // of the 16 dimension tiles is followed by a piece of other work, and the
     // operands are read four tiles ahead
     auto value_wide = [&](uint32_t base, auto&& between) {
       if constexpr (S::kWide) {
-        constexpr int kRing = 5;
+        constexpr int kRing = 6;
         s16x8 v[kRing][2];
+        uint32_t at[4];  // even and odd dimension tile, first and second half of 16 keys
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = opaque(base + (v_at ^ ((i & 1) * 64) ^ ((i >> 1) * 32)));
         auto read = [&](int d) {
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            const uint32_t va = base + (v_at ^ ((d & 1) * 64)) + (2 * kk) * kOctBytes + (d >> 1) * 1024;
-            const uint32_t vb = base + (v_at ^ ((d & 1) * 64) ^ 32) + (2 * kk + 1) * kOctBytes + (d >> 1) * 1024;
-            v[d % kRing][kk] = __builtin_shufflevector(lds_read_tr(va), lds_read_tr(vb), 0, 1, 2, 3, 4, 5, 6, 7);
-          }
+          for (int kk = 0; kk < 2; ++kk)
+            v[d % kRing][kk] =
+                __builtin_shufflevector(lds_read_tr(at[d & 1] + (2 * kk) * kOctBytes + (d >> 1) * 1024),
+                                        lds_read_tr(at[2 + (d & 1)] + (2 * kk + 1) * kOctBytes + (d >> 1) * 1024), 0, 1,
+                                        2, 3, 4, 5, 6, 7);
         };
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int d = 0; d < kRing - 1; ++d) read(d);
+        for (int d = 0; d < kRing - 2; ++d) read(d);
 #pragma unroll
         for (int d = 0; d < kAccs; d += 2) {
+          if (d + kRing - 2 < kAccs) read(d + kRing - 2);
           __builtin_amdgcn_sched_barrier(0);
-          E::mfma_acc(v[d % kRing][0], p_wide[0], acc[d]);
-          if (d + kRing - 1 < kAccs) read(d + kRing - 1);
+          E::mfma_acc(v[d % kRing][0], v[(d + 1) % kRing][0], __builtin_bit_cast(s16x8, p_wide[0]), acc[d],
+                      acc[d + 1]);
           between(d);
           __builtin_amdgcn_sched_barrier(0);
-          E::mfma_acc(v[(d + 1) % kRing][0], p_wide[0], acc[d + 1]);
-          E::mfma_acc(v[d % kRing][1], p_wide[1], acc[d]);
-          between(d + 1);
+          if (d + kRing - 1 < kAccs) read(d + kRing - 1);
           __builtin_amdgcn_sched_barrier(0);
-          E::mfma_acc(v[(d + 1) % kRing][1], p_wide[1], acc[d + 1]);
-          if (d + kRing < kAccs) read(d + kRing);
+          E::mfma_acc(v[d % kRing][1], v[(d + 1) % kRing][1], __builtin_bit_cast(s16x8, p_wide[1]), acc[d],
+                      acc[d + 1]);
+          between(d + 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -740,21 +824,29 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     auto do_step = [&](int step) -> bool {
       // the step's keys are in their slot, and every wave has left the slot
       // that the next issue fills
-      if (S::kDistance == 2 && step + 1 < step_end)
-        wait_and_barrier<S::kOctets * kOctLoads>();
-      else
+      if constexpr (S::kWide) {
+        wait_and_barrier<S::kOctets * kOctLoads>();  // all but the next step's
+        locate(step + S::kDistance);
+      } else {
         wait_and_barrier<0>();
-      if (step + S::kDistance < step_end) issue(step + S::kDistance);
+        if (step + S::kDistance < step_end) issue(step + S::kDistance);
+      }
       const int slot = (step - step0) & (S::kSlots - 1);
       const uint32_t base = ring + slot * S::kSlotBytes + (S::kWide ? 0 : ts * ST * kBlkBytes);
 
       // ---- S = K Q^T
       float z[kScores];
       if constexpr (S::kWide) {
-        f32x16 s0 = {}, s1 = {};  // two chains
-        constexpr int kRing = 8;  // operands: 6 read ahead
+        // Between the MFMAs: the loads of the step after next and the weights
+        // of the step before.
+        f32x16 s0 = {};
+        float sum = 0.0f;
+        constexpr int kRing = 6;  // operands: 4 read ahead
         s16x8 kk[kRing];
-        auto read = [&](int ks) { kk[ks % kRing] = lds_read(base + (k_at ^ ((ks & 3) * 32)) + (ks >> 2) * 1024); };
+        uint32_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = opaque(base + (k_at ^ (i * 32)));
+        auto read = [&](int ks) { kk[ks % kRing] = lds_read(at[ks & 3] + (ks >> 2) * 1024); };
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ks = 0; ks < kRing - 2; ++ks) read(ks);
@@ -765,11 +857,16 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
             if (ks + kRing - 2 + i < kQ) read(ks + kRing - 2 + i);
           __builtin_amdgcn_sched_barrier(0);
           s0 = E::mfma_wide(kk[ks % kRing], q[ks], s0);
-          s1 = E::mfma_wide(kk[(ks + 1) % kRing], q[ks + 1], s1);
+          s0 = E::mfma_wide(kk[(ks + 1) % kRing], q[ks + 1], s0);
+          if (ks / 2 < kOctLoads)
+            load_one(ks / 2);
+          else if (ks / 2 - kOctLoads < 8)
+            weigh(ks / 2 - kOctLoads, sum);
           __builtin_amdgcn_sched_barrier(0);
         }
+        l += sum;
 #pragma unroll
-        for (int i = 0; i < kScores; ++i) z[i] = s0[i] + s1[i];
+        for (int i = 0; i < kScores; ++i) z[i] = s0[i];
       } else {
         constexpr int kChains = ST == 1 ? 2 : 1;
         constexpr int kReads = kKSteps * ST, kRing = 8;
@@ -808,20 +905,21 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       };
       const int step_key = step * S::kKeys;  // of the item's list
       if (a.softcap > 0.0f) {
-        const float by = a.scale / a.softcap, cap = a.softcap * kLog2e;
+        const float in = a.scale / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
-        for (int i = 0; i < kScores; ++i) z[i] = cap * tanh_f32(z[i] * by);
-      } else {
+        for (int i = 0; i < kScores; ++i) z[i] = cap * tanh_f32(z[i] * in);
+      } else if (!S::kWide || prescale) {
 #pragma unroll
         for (int i = 0; i < kScores; ++i) z[i] *= to_log2;
       }
       if (a.slopes) {
+        const PairInfo info = s_pair[pg * S::kWavePairs + col];
         const int32_t* list = KIND == kSparse ? a.indices + static_cast<int64_t>(it.row0) * a.k : nullptr;
 #pragma unroll
         for (int i = 0; i < kScores; ++i) {
           const int c = step_key + key_of(i);
           const int tok = KIND == kSparse ? list[min(c, a.k - 1)] : it.tile0 * kTile + c;
-          z[i] -= p_slope * fabsf(static_cast<float>(p_pos - tok));
+          z[i] -= info.slope * fabsf(static_cast<float>(info.pos - tok));
         }
       }
       bool mixed = false;  // some key that was read is hidden from some row
@@ -846,23 +944,14 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         const int first = it.tile0 * kTile + step_key;
         mixed = max(first, it.min_start) < it.max_start || min(first + S::kKeys, it.max_end) > it.min_end;
         if (first < it.max_start || first + S::kKeys > it.min_end) {
+          const PairInfo info = s_pair[pg * S::kWavePairs + col];
 #pragma unroll
           for (int i = 0; i < kScores; ++i) {
             const int tok = first + key_of(i);
-            z[i] = tok >= p_start && tok < p_end ? z[i] : -__builtin_inff();
+            z[i] = tok >= info.start && tok < info.end ? z[i] : -__builtin_inff();
           }
         }
       }
-
-      // ---- running maximum: raised where a score passes it by kRaise
-      float mx = z[0];
-#pragma unroll
-      for (int i = 1; i < kScores; ++i) mx = fmaxf(mx, z[i]);
-      mx = pair_max<S::kWide>(mx) - E::kShift;
-      const float raised = mx > m + E::kRaise ? mx : m;
-      const bool any_raised = step > step0 && __ballot(raised != m) != 0;  // nothing to rescale in the first step
-      by = __builtin_amdgcn_exp2f(m - raised);
-      m = raised;
 
       // A key that some rows of the pair tile see and others do not may hold an
       // infinity or a NaN; a weight of zero would not take it out of the
@@ -884,23 +973,33 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       }
 
       if constexpr (S::kWide) {
-        // ---- the step before: O^T += V^T P^T, with this step's exponentials
-        // between its MFMAs; then the accumulators take the new maximum
-        // (the first step has none before it: weights of zero on its own keys,
-        // which every row of the pair tile sees or whose non-finite values
-        // have just been cleared)
-        s16x8 p_next[2];
-        float sum = 0.0f;
-        value_wide(step > step0 ? ring + ((step - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes : base, [&](int i) {
-          const float e = __builtin_amdgcn_exp2f(z[i] - m);
-          sum += e;
-          p_next[i / 8][i % 8] = E::round(e);
+        // ---- the step before: O^T += V^T P^T, with this step's maximum between
+        // its MFMAs; then the accumulators take it.  (The first step has none
+        // before it: weights of zero on its own keys, which every row of the
+        // pair tile sees or whose non-finite values have been cleared.)
+        float mx = -__builtin_inff();
+        value_wide(step > step0 ? ring + ((step - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes : base, [&](int d) {
+          if (d < 8) mx = fmaxf(mx, fmaxf(z[2 * d], z[2 * d + 1]));
         });
-        p_wide[0] = p_next[0];
-        p_wide[1] = p_next[1];
-        l = l * by + sum;
+        mx = pair_max<true>(mx) * z_scale - E::kShift;
+        const float raised = mx > m + E::kRaise ? mx : m;
+        const bool any_raised = step > step0 && __ballot(raised != m) != 0;  // nothing to rescale in the first step
+        by = __builtin_amdgcn_exp2f(m - raised);
+        m = raised;
+        l *= by;
+#pragma unroll
+        for (int i = 0; i < kScores; ++i) z_before[i] = z[i];
         return any_raised;
       } else {
+        // ---- running maximum: raised where a score passes it by kRaise
+        float mx = z[0];
+#pragma unroll
+        for (int i = 1; i < kScores; ++i) mx = fmaxf(mx, z[i]);
+        mx = pair_max<false>(mx) - E::kShift;
+        const float raised = mx > m + E::kRaise ? mx : m;
+        const bool any_raised = step > step0 && __ballot(raised != m) != 0;  // nothing to rescale in the first step
+        by = __builtin_amdgcn_exp2f(m - raised);
+        m = raised;
         if (any_raised) {
           l *= by;
 #pragma unroll
@@ -972,22 +1071,47 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       }
 #pragma unroll
       for (int d = 0; d < kAccs; ++d) pin(acc[d]);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) weigh(i, sum);
+      l += sum;
       value_wide(ring + ((step_end - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes, [](int) {});
     } else {
       for (int step = step0; step < step_end; ++step) do_step(step);
     }
 
-    // ---- the streams' parts of each pair become one, 128 dimensions at a
-    // time through LDS, and leave as whole rows
+    // ---- the streams' parts of each pair become one, through LDS, and leave as
+    // whole rows
     {
       const float sum = pair_sum<S::kWide>(l);
       if (lane < S::kWavePairs) s_ml[wave][lane] = make_float2(m, sum);
     }
-    lds_barrier();  // every wave has left the last step, and s_ml is complete
+    wait_and_barrier<0>();  // every wave has left the ring, its last loads have ended, and s_ml is complete
     float* piece = nullptr;
     if (!whole) {
       const int64_t id = KIND == kShared ? static_cast<int64_t>(w) + item : (lo == 0 ? 2 * w + 1 : 2 * w);
       piece = pieces + id * piece_floats(M);
+    }
+    float factor = 0.0f;  // of this lane's part of its pair
+    {
+      const int first = pg * S::kStreams;
+      float top = kMInit, sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < S::kStreams; ++k) top = fmaxf(top, s_ml[first + k][col].x);
+#pragma unroll
+      for (int k = 0; k < S::kStreams; ++k) {
+        const float2 ml = s_ml[first + k][col];
+        sum += ml.y * __builtin_amdgcn_exp2f(ml.x - top);
+      }
+      factor = __builtin_amdgcn_exp2f(m - top);
+      const int local = pg * S::kWavePairs + col;
+      if (whole) {
+        factor = sum == 0.0f ? 0.0f : factor / sum;
+        if (a.lse && ts == 0 && lane < S::kWavePairs && local < it.pairs)
+          a.lse[pair_base + local] = (top + __log2f(sum)) * kLn2;
+      } else if (ts == 0 && lane < S::kWavePairs && local < it.pairs) {
+        reinterpret_cast<float2*>(piece + M * kValDim)[local] = make_float2(top, sum);
+      }
     }
     // 64 (narrow) or 128 (wide) rows of accumulators; the pad of 4 floats
     // spreads the pairs over all banks
@@ -1004,44 +1128,28 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<f32x4*>(mine + (d & 7) * 32 + 8 * i + 4 * half) =
-                f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+                f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]} * factor;
         }
       } else {
 #pragma unroll
         for (int d = 0; d < kAccs; ++d) {
-          if constexpr (!S::kWide) *reinterpret_cast<f32x4*>(mine + d * 16 + 4 * g4) = acc[d];
+          if constexpr (!S::kWide) *reinterpret_cast<f32x4*>(mine + d * 16 + 4 * g4) = acc[d] * factor;
         }
       }
       lds_barrier();
-#pragma unroll 2
-      for (int i = tid; i < it.pairs * (kChunkDims / 4); i += kAttnThreads) {
-        const int local = i / (kChunkDims / 4), dim = (i % (kChunkDims / 4)) * 4;
-        const int group = local / S::kWavePairs, in = local % S::kWavePairs;
-        float top = kMInit;
+      constexpr int kPerRow = kChunkDims / 4, kRows = kAttnThreads / kPerRow;  // rows at a time
+      const int dim = tid % kPerRow * 4;
+#pragma unroll 4
+      for (int local = tid / kPerRow; local < it.pairs; local += kRows) {
+        const float* parts = s_o + (local / S::kWavePairs * S::kStreams * S::kWavePairs + local % S::kWavePairs) * kStride + dim;
+        f32x4 o = *reinterpret_cast<const f32x4*>(parts);
 #pragma unroll
-        for (int k = 0; k < S::kStreams; ++k) top = fmaxf(top, s_ml[group * S::kStreams + k][in].x);
-        f32x4 o = {0, 0, 0, 0};
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < S::kStreams; ++k) {
-          const int from = group * S::kStreams + k;
-          const float2 ml = s_ml[from][in];
-          const float part = S::kStreams == 1 ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
-          sum += ml.y * part;
-          o += *reinterpret_cast<const f32x4*>(s_o + (from * S::kWavePairs + in) * kStride + dim) * part;
-        }
+        for (int k = 1; k < S::kStreams; ++k) o += *reinterpret_cast<const f32x4*>(parts + k * S::kWavePairs * kStride);
         if (whole) {
-          const int64_t pair = pair_base + local;
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          s16x4 r;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) r[j] = E::round(o[j] * inv);
-          *reinterpret_cast<s16x4*>(static_cast<short*>(a.out) + pair * kValDim + c * kChunkDims + dim) = r;
-          if (a.lse && c == 0 && dim == 0) a.lse[pair] = (top + __log2f(sum)) * kLn2;
+          const int2 r = make_int2(E::round2(o[0], o[1]), E::round2(o[2], o[3]));
+          *reinterpret_cast<int2*>(static_cast<short*>(a.out) + (pair_base + local) * kValDim + c * kChunkDims + dim) = r;
         } else {
           *reinterpret_cast<f32x4*>(piece + static_cast<int64_t>(local) * kValDim + c * kChunkDims + dim) = o;
-          if (c == 0 && dim == 0)
-            reinterpret_cast<float2*>(piece + M * kValDim)[local] = make_float2(top, sum);
         }
       }
     }
