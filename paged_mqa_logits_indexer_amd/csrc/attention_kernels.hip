@@ -826,7 +826,6 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       // that the next issue fills
       if constexpr (S::kWide) {
         wait_and_barrier<S::kOctets * kOctLoads>();  // all but the next step's
-        locate(step + S::kDistance);
       } else {
         wait_and_barrier<0>();
         if (step + S::kDistance < step_end) issue(step + S::kDistance);
@@ -850,6 +849,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ks = 0; ks < kRing - 2; ++ks) read(ks);
+        __builtin_amdgcn_sched_barrier(0);
+        locate(step + S::kDistance);  // while they come
 #pragma unroll
         for (int ks = 0; ks < kQ; ks += 2) {
 #pragma unroll
@@ -1180,6 +1181,8 @@ struct Joined {
   float m, l;
 };
 
+constexpr int kAtOnce = 8;  // pieces whose loads are in flight together
+
 // Adds n pieces: 64 at a time, first their maxima and sums (one lane each),
 // then their rows, whose loads do not wait for one another.
 template <class At>
@@ -1201,12 +1204,22 @@ __device__ __forceinline__ void join_list(Joined& j, int n, int M, int local, At
     j.o0 *= mine;
     j.o1 *= mine;
     const int some = min(n - i0, kWave);
-#pragma unroll 8
-    for (int i = 0; i < some; ++i) {
-      const f32x4* o = reinterpret_cast<const f32x4*>(at(i0 + i) + static_cast<int64_t>(local) * kValDim + lane * 8);
-      const float by = __shfl(part, i);
-      j.o0 += o[0] * by;
-      j.o1 += o[1] * by;
+    // (every lane: piece 0 for those past the end, with weight 0)
+    for (int i = 0; i < some; i += kAtOnce) {
+      f32x4 a[kAtOnce], b[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const f32x4* o = reinterpret_cast<const f32x4*>(at(i0 + min(i + k, some - 1)) +
+                                                        static_cast<int64_t>(local) * kValDim + lane * 8);
+        a[k] = o[0];
+        b[k] = o[1];
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float by = i + k < some ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(part), i + k)) : 0.0f;
+        j.o0 += a[k] * by;
+        j.o1 += b[k] * by;
+      }
     }
   }
 }
