@@ -1273,16 +1273,60 @@ __global__ __launch_bounds__(256) void join_shared_kernel(JoinArgs a, int M, int
   write_joined<DT>(j, pair, a.out, a.lse);
 }
 
-// Pairs of a pair tile, by the pairs that one request brings (its rows' heads):
-// as few idle matrix columns as possible.
-int tile_pairs(int64_t pairs_per_request) {
-  return pairs_per_request <= 16 ? 16 : pairs_per_request <= 32 ? 32 : pairs_per_request <= 64 ? 64 : 128;
-}
-
 constexpr int kMaxGrid = 256;  // one persistent workgroup per CU
 constexpr int kMinUnits = kItemCost + 2;  // smallest share: below, the join costs more than the split saves
 
 size_t join_bytes(int64_t infos) { return (static_cast<size_t>(infos) * sizeof(JoinInfo) + 255) / 256 * 256; }
+
+// Pairs that one request (sparse: one row; shared: the batch, for the prefix)
+// brings together.
+template <int KIND>
+int64_t pairs_together(const AttentionArgs& a) {
+  if (KIND == kSparse) return a.heads;
+  if (KIND == kShared) return static_cast<int64_t>(a.rows) * a.heads;
+  return (static_cast<int64_t>(a.rows) + a.requests - 1) / a.requests * a.heads;
+}
+
+// Size of the pair tiles: the one whose estimated time is least.  A workgroup
+// spends kPerTile on each of its shares of the 64-key tiles and kFixed on the
+// call (start, queries, output, and the float32 pieces of pair tiles that are
+// split, 2 KiB per pair and workgroup, written and joined).  Microseconds, from
+// every size forced on selections of 512 and 2048 keys for 1 .. 256 rows of 32,
+// 64 and 128 heads, and on 1 .. 64 requests of 256 .. 32768 keys with 16 .. 128
+// heads.  Between them (16 / 32 / 64 / 128 pairs): 8 rows of 128 heads over
+// 2048 keys 31 / 29 / 36 / 46 us, 64 rows 123 / 80 / 96 / 103, 256 rows 689 /
+// 367 / 296 / 203; 64 heads, 256 rows 354 / 188 / 152 / 180; 16 requests of
+// 8192 keys with 128 heads 112 / 85 / 103 / 121, of 32768 keys 396 / 265 / 268
+// / 221.  (For whole pages the table's width stands for the lengths, which the
+// host does not know.)  Tiles wider than the pairs would only idle.
+template <int KIND>
+int tile_pairs(const AttentionArgs& a) {
+  constexpr int kSizes[] = {16, 32, 64, 128};
+  constexpr double kPerTile[] = {2.2, 2.1, 3.5, 3.9}, kFixed[] = {19, 20, 32, 65};
+  const int64_t together = pairs_together<KIND>(a);
+  int best = 16;
+  double least = 1e300;
+  for (int i = 0; i < 4; ++i) {
+    const int m = kSizes[i];
+    if (i > 0 && together <= m / 2) break;
+    const int64_t pairs = static_cast<int64_t>(a.rows) * a.heads;
+    double tiles;
+    if (KIND == kSparse) {
+      tiles = static_cast<double>(a.rows) * ((a.heads + m - 1) / m) * ((a.k + kTile - 1) / kTile);
+    } else {
+      const double own = a.cu_q ? static_cast<double>(pairs / m + a.requests)
+                                : static_cast<double>(a.requests) * ((static_cast<int64_t>(a.next_n) * a.heads + m - 1) / m);
+      tiles = KIND == kShared ? static_cast<double>((pairs + m - 1) / m) * a.prefix_pages + own * (a.max_pages - a.prefix_pages)
+                              : own * a.max_pages;
+    }
+    const double t = tiles / kMaxGrid * kPerTile[i] + kFixed[i];
+    if (t < least) {
+      least = t;
+      best = m;
+    }
+  }
+  return best;
+}
 
 template <int DT, int KIND, int M>
 hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
@@ -1310,9 +1354,7 @@ hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
 
 template <int DT, int KIND>
 hipError_t launch_kind(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
-  const int64_t per_request = KIND == kSparse ? a.heads
-                                              : (static_cast<int64_t>(a.rows) + a.requests - 1) / a.requests * a.heads;
-  switch (tile_pairs(per_request)) {
+  switch (tile_pairs<KIND>(a)) {
     case 16: return launch<DT, KIND, 16>(a, stream, ev);
     case 32: return launch<DT, KIND, 32>(a, stream, ev);
     case 64: return launch<DT, KIND, 64>(a, stream, ev);
@@ -1328,20 +1370,24 @@ hipError_t launch_type(const AttentionArgs& a, hipStream_t stream, LaunchEvents 
 
 }  // namespace
 
+// For any size of the pair tiles that the calls may take: the queries do not
+// know the keys.
 size_t attention_workspace_size(int32_t rows, int32_t heads, int32_t requests) {
   if (rows <= 0 || heads <= 0 || requests <= 0) return 0;
-  // whichever of the operators that share this query needs more
-  const int64_t per_request = (static_cast<int64_t>(rows) + requests - 1) / requests * heads;
-  const int m = std::max(tile_pairs(per_request), tile_pairs(heads));
+  const int64_t together = (static_cast<int64_t>(rows) + requests - 1) / requests * heads;
+  const int m = together <= 16 ? 16 : together <= 32 ? 32 : together <= 64 ? 64 : 128;
   return join_bytes(kMaxGrid) + 2 * kMaxGrid * static_cast<size_t>(piece_floats(m)) * sizeof(float);
 }
 
 size_t shared_prefix_workspace_size(int32_t rows, int32_t heads, int32_t requests) {
   if (rows <= 0 || heads <= 0 || requests <= 0) return 0;
   const int64_t per_request = (static_cast<int64_t>(rows) + requests - 1) / requests * heads;
-  const int m = tile_pairs(per_request);
-  const int64_t items = (static_cast<int64_t>(rows) * heads + m - 1) / m + requests * ((per_request + m - 1) / m);
-  return join_bytes(items) + (items + kMaxGrid) * static_cast<size_t>(piece_floats(m)) * sizeof(float);
+  size_t most = 0;
+  for (int m = 16; m <= 128; m *= 2) {
+    const int64_t items = (static_cast<int64_t>(rows) * heads + m - 1) / m + requests * ((per_request + m - 1) / m);
+    most = std::max(most, join_bytes(items) + (items + kMaxGrid) * static_cast<size_t>(piece_floats(m)) * sizeof(float));
+  }
+  return most;
 }
 
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
