@@ -416,12 +416,18 @@ struct Share {
   int64_t item_at;     // unit offset of `item`
   int item;
   int groups;          // workgroups with work
+  int cost;            // units that an item counts for beside its tiles
 };
 
 // Taking up a pair tile and writing it costs about as much as kItemCost tiles
-// of keys: a pair tile counts for that many more, at its beginning.
-constexpr int kItemCost = 3;
-__device__ __forceinline__ int item_units(const Item& it) { return it.tiles ? it.tiles + kItemCost : 0; }
+// of keys: a pair tile counts for that many more, at its beginning.  (64
+// requests of 1 .. 32768 keys 162 -> 78 us against 0; 5 and 8 measure 2 and 1 us
+// slower there, but the wide form writes more: 109 -> 105 and 130 -> 117 us for
+// ragged extends and 8 requests on a shared prefix with 6 instead of 3.)
+template <int M>
+constexpr int kItemCost = M == 128 ? 6 : 3;
+template <int M>
+__device__ __forceinline__ int item_units(const Item& it) { return it.tiles ? it.tiles + kItemCost<M> : 0; }
 
 // Share of workgroup w: as many groups as give each min_units.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int groups, int w) {
@@ -435,22 +441,40 @@ __device__ __forceinline__ int share_owner(int64_t total, int groups, int64_t t)
   return w;
 }
 
+// min_units 0 (sparse lists of few rows): every item is cut into grid / items
+// equal parts, so that a workgroup has one of them, and items cost nothing.
 template <int KIND, int M>
 __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_units, int* s_scan, int64_t* s_res) {
   Share s;
   const int items = static_cast<int>(item_count<KIND, M>(a));
   const int tid = threadIdx.x;
+  s.cost = kItemCost<M>;
   if constexpr (KIND == kSparse) {
     if (!a.cu_q) {
-      const int n = (a.k + kTile - 1) / kTile + kItemCost;
+      if (min_units == 0) s.cost = 0;
+      const int n = (a.k + kTile - 1) / kTile + s.cost;
       s.total = static_cast<int64_t>(items) * n;
-      s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_units)));
+      s.groups = min_units == 0
+                     ? grid
+                     : static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_units)));
       s.t0 = w < s.groups ? share_begin(s.total, s.groups, w) : 0;
       s.t1 = w < s.groups ? share_begin(s.total, s.groups, w + 1) : 0;
       s.item = static_cast<int>(s.t0 / n);
       s.item_at = static_cast<int64_t>(s.item) * n;
       return s;
     }
+  }
+  if (items <= kWave) {
+    // few items: every wave by itself, an item per lane
+    const int n = lane_id() < items ? item_units<M>(make_item<KIND, M, 1>(a, lane_id())) : 0;
+    const int upto = wave_inclusive_scan(n);
+    s.total = __builtin_amdgcn_readlane(upto, kWave - 1);
+    s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_units)));
+    s.t0 = w < s.groups ? share_begin(s.total, s.groups, w) : 0;
+    s.t1 = w < s.groups ? share_begin(s.total, s.groups, w + 1) : 0;
+    s.item = first_lane(__ballot(upto > s.t0));
+    s.item_at = __builtin_amdgcn_readlane(upto, s.item) - __builtin_amdgcn_readlane(n, s.item);
+    return s;
   }
   // Tiles per chunk of 256 items, then their sum, then the chunk that holds t0
   // is walked again.  s_scan: a counter per wave, then the chunk sums.
@@ -460,7 +484,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   int n = 0;
   for (int c = 0; c < chunks; ++c) {
     const int id = c * kAttnThreads + tid;
-    n = id < items ? item_units(make_item<KIND, M, 1>(a, id)) : 0;
+    n = id < items ? item_units<M>(make_item<KIND, M, 1>(a, id)) : 0;
     const int sum = wave_sum(n);
     if (lane_id() == 0) s_wave[tid / kWave] = sum;
     __syncthreads();
@@ -483,7 +507,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   int c = 0;
   while (c + 1 < chunks && at + s_chunk[c] <= s.t0) at += s_chunk[c++];
   const int id = c * kAttnThreads + tid;
-  if (c + 1 < chunks) n = id < items ? item_units(make_item<KIND, M, 1>(a, id)) : 0;
+  if (c + 1 < chunks) n = id < items ? item_units<M>(make_item<KIND, M, 1>(a, id)) : 0;
   const int upto = wave_inclusive_scan(n);
   if (lane_id() == kWave - 1) s_wave[tid / kWave] = upto;
   __syncthreads();
@@ -599,8 +623,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   int item = share.item;
   for (; at < share.t1 && item < items; ++item) {
     const Item it = make_item<KIND, M, kWave>(a, item);
-    const int64_t tiles_at = item_at + (it.tiles ? kItemCost : 0);
-    item_at += item_units(it);
+    const int64_t tiles_at = item_at + (it.tiles ? share.cost : 0);
+    item_at = tiles_at + it.tiles;
     const int lo = static_cast<int>(max(int64_t{0}, at - tiles_at));
     const int hi = static_cast<int>(min(static_cast<int64_t>(it.tiles), share.t1 - tiles_at));
     at = item_at;
@@ -780,10 +804,12 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
 
     // the value product of one step (wide), V^T P^T on the keys at `base`; each
     // of the 16 dimension tiles is followed by a piece of other work, and the
-    // operands are read four tiles ahead
+    // operands are read two tiles ahead (four, or the first ones before the
+    // scores: 118 -> 130 us for 8 requests on 32768 shared keys; there are no
+    // registers for them)
     auto value_wide = [&](uint32_t base, auto&& between) {
       if constexpr (S::kWide) {
-        constexpr int kRing = 6;
+        constexpr int kRing = 4;
         s16x8 v[kRing][2];
         uint32_t at[4];  // even and odd dimension tile, first and second half of 16 keys
 #pragma unroll
@@ -1155,7 +1181,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       }
     }
     if (!whole && lo == 0 && tid == 0) {
-      const int last = share_owner(share.total, share.groups, tiles_at + it.tiles - 1);
+      const int last = share_owner(share.total, share.groups, item_at - 1);
       JoinInfo j;
       j.pair0 = pair_base;
       j.pairs = it.pairs;
@@ -1228,27 +1254,50 @@ template <int DT>
 __device__ __forceinline__ void write_joined(const Joined& j, int64_t pair, void* out, float* lse) {
   using E = Elem<DT>;
   const float inv = j.l == 0.0f ? 0.0f : 1.0f / j.l;
-  s16x8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = E::round(j.o0[i] * inv);
-    r[4 + i] = E::round(j.o1[i] * inv);
-  }
-  *reinterpret_cast<s16x8*>(static_cast<short*>(out) + pair * kValDim + lane_id() * 8) = r;
+  const i32x4 r = {E::round2(j.o0[0] * inv, j.o0[1] * inv), E::round2(j.o0[2] * inv, j.o0[3] * inv),
+                   E::round2(j.o1[0] * inv, j.o1[1] * inv), E::round2(j.o1[2] * inv, j.o1[3] * inv)};
+  *reinterpret_cast<i32x4*>(static_cast<short*>(out) + pair * kValDim + lane_id() * 8) = r;
   if (lse && lane_id() == 0) lse[pair] = (j.m + __log2f(j.l)) * kLn2;
 }
 
-// Dense and sparse: block (w, y) joins pairs 4 y .. 4 y + 3 of the pair tile
-// that workgroup w began and others went on with.
-template <int DT>
+// Dense and sparse: block (x, w) joins pairs of the pair tile that workgroup w
+// began and others went on with: pairs 4 x .. 4 x + 3, one wave each, or (SPREAD)
+// pair x, its pieces dealt to the four waves -- few pairs have many pieces each,
+// and the loads of a wave are one round trip per kAtOnce pieces.  (Pairs on x:
+// blocks are dealt to the 8 XCDs in turn, and the workgroups that begin a tile
+// are often every eighth; with them on x all work fell on one XCD, 16 instead
+// of 6 us for 8 rows over 2048 keys.)
+template <int DT, bool SPREAD>
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs a, int M) {
-  const JoinInfo info = a.info[blockIdx.x];
-  const int local = blockIdx.y * 4 + static_cast<int>(threadIdx.x >> 6);
+  __shared__ f32x4 s_o[SPREAD ? 4 : 1][2][kWave];
+  __shared__ float2 s_ml[4];
+  const JoinInfo info = a.info[blockIdx.y];
+  const int wave = threadIdx.x >> 6, lane = lane_id();
+  const int local = SPREAD ? blockIdx.x : blockIdx.x * 4 + wave;
   if (info.pieces == 0 || local >= info.pairs) return;
+  constexpr int kBy = SPREAD ? 4 : 1;
+  const int skip = SPREAD ? wave : 0;
   Joined j{{0, 0, 0, 0}, {0, 0, 0, 0}, kMInit, 0.0f};
-  join_list(j, info.pieces, M, local, [&](int i) {
-    return a.pieces + static_cast<int64_t>(i == 0 ? 2 * info.first + 1 : 2 * (info.first + i)) * piece_floats(M);
+  join_list(j, (info.pieces - skip + kBy - 1) / kBy, M, local, [&](int i) {
+    const int piece = i * kBy + skip;
+    return a.pieces + static_cast<int64_t>(piece == 0 ? 2 * info.first + 1 : 2 * (info.first + piece)) * piece_floats(M);
   });
+  if constexpr (SPREAD) {
+    s_o[wave][0][lane] = j.o0;
+    s_o[wave][1][lane] = j.o1;
+    if (lane == 0) s_ml[wave] = make_float2(j.m, j.l);
+    __syncthreads();
+    if (wave) return;
+    for (int k = 1; k < 4; ++k) {
+      const float2 ml = s_ml[k];
+      const float top = fmaxf(j.m, ml.x);
+      const float mine = __builtin_amdgcn_exp2f(j.m - top), theirs = __builtin_amdgcn_exp2f(ml.x - top);
+      j.o0 = j.o0 * mine + s_o[k][0][lane] * theirs;
+      j.o1 = j.o1 * mine + s_o[k][1][lane] * theirs;
+      j.l = j.l * mine + ml.y * theirs;
+      j.m = top;
+    }
+  }
   write_joined<DT>(j, info.pair0 + local, a.out, a.lse);
 }
 
@@ -1274,7 +1323,9 @@ __global__ __launch_bounds__(256) void join_shared_kernel(JoinArgs a, int M, int
 }
 
 constexpr int kMaxGrid = 256;  // one persistent workgroup per CU
-constexpr int kMinUnits = kItemCost + 2;  // smallest share: below, the join costs more than the split saves
+constexpr int kMinTiles = 2;   // smallest part of an item that is cut into equal ones
+template <int M>
+constexpr int kMinUnits = kItemCost<M> + 2;  // smallest share: below, the join costs more than the split saves
 
 size_t join_bytes(int64_t infos) { return (static_cast<size_t>(infos) * sizeof(JoinInfo) + 255) / 256 * 256; }
 
@@ -1332,13 +1383,19 @@ template <int DT, int KIND, int M>
 hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
   const int64_t items = item_count<KIND, M>(a);
   const int64_t tiles = KIND == kSparse ? (a.k + kTile - 1) / kTile : a.max_pages;
-  const int grid = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + kItemCost) / kMinUnits)));
+  int grid = static_cast<int>(
+      std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + kItemCost<M>) / kMinUnits<M>)));
+  int min_units = kMinUnits<M>;
+  if (KIND == kSparse && !a.cu_q && items <= kMaxGrid / 2) {  // parts of one item each
+    grid = static_cast<int>(items * std::min<int64_t>(kMaxGrid / items, std::max<int64_t>(1, tiles / kMinTiles)));
+    min_units = 0;
+  }
   JoinInfo* info = static_cast<JoinInfo*>(a.workspace);
   float* pieces = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
                                            join_bytes(KIND == kShared ? items : kMaxGrid));
   const bool joins = KIND == kShared || grid > 1;
   launch_kernel(attention_kernel<DT, KIND, M>, dim3(grid), dim3(kAttnThreads), stream, ev.start,
-                joins ? nullptr : ev.stop, a, kMinUnits, info, pieces);
+                joins ? nullptr : ev.stop, a, min_units, info, pieces);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !joins) return e;
   const JoinArgs j{info, pieces, a.out, a.lse};
@@ -1347,7 +1404,12 @@ hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
     launch_kernel(join_shared_kernel<DT>, dim3(static_cast<uint32_t>((pairs + 3) / 4)), dim3(256), stream, nullptr,
                   ev.stop, j, M, pairs, a.heads, a.next_n);
   } else {
-    launch_kernel(join_kernel<DT>, dim3(grid, M / 4), dim3(256), stream, nullptr, ev.stop, j, M);
+    // (at 16 pairs, 14 -> 7 us where requests of up to 32768 keys have up to 35
+    // pieces; at 32 pairs and 8 pieces 6 -> 7 us)
+    if (M == 16)
+      launch_kernel(join_kernel<DT, true>, dim3(M, grid), dim3(256), stream, nullptr, ev.stop, j, M);
+    else
+      launch_kernel(join_kernel<DT, false>, dim3(M / 4, grid), dim3(256), stream, nullptr, ev.stop, j, M);
   }
   return hipGetLastError();
 }
