@@ -597,52 +597,53 @@ def score_histogram(scores, context_lens, hist):
     _check("score_histogram", st)
 
 
+_entry_points: dict = {}
+
+
 def _launch(name, dev, events, *args):
     """One call of the C entry point on the current stream of ``dev``."""
-    fn = getattr(load_library(), name)
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(load_library(), name)
     if dev.index == torch.cuda.current_device():
-        _arm(events, dev)
+        if events is not None:
+            _arm(events, dev)
         st = fn(*args, _stream_ptr(dev))
     else:
         with torch.cuda.device(dev):
             _arm(events, dev)
             st = fn(*args, _stream_ptr(dev))
-    _check(name, st)
+    if st:
+        _check(name, st)
 
 
-def _need_flat(t, name, dtype, dev, n):
-    """A contiguous [n] tensor of ``dtype`` on ``dev``."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == dev and t.is_cuda and
-            t.shape == (n,) and t.is_contiguous()):
-        _need(t, name, dtype, dev, 1)
-        raise ValueError(f"{name} must be contiguous [{n}]")
+def _need_shaped(t, name, dtype, dev, shape):
+    """A contiguous tensor of ``dtype`` and ``shape`` on ``dev``.  The calls of a
+    decode step take longer on the host than on the GPU, so what holds is seen
+    in one condition and only what does not is looked into."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and
+            t.is_contiguous() and t.device == dev):
+        _need(t, name, dtype, dev, len(shape))
+        raise ValueError(f"{name} must be contiguous {list(shape)}")
 
 
 def _append_call(name, dim, dtypes, rows, positions, slots, rope, pages, tail, interleaved, events):
-    dev = rows.device
-    if rows.dtype not in dtypes:
-        raise TypeError(f"rows must be one of {dtypes}, got {rows.dtype}")
-    _need(rows, "rows", rows.dtype, dev, 2)
+    dev, dtype = rows.device, rows.dtype
+    if dtype not in dtypes:
+        raise TypeError(f"rows must be one of {dtypes}, got {dtype}")
+    _need(rows, "rows", dtype, dev, 2)
     tokens, width = rows.shape
     stride, unit = rows.stride()
     if width != dim or unit != 1:
         raise ValueError(f"rows must be [tokens, {dim}] with unit column stride")
     if tokens == 1:
         stride = dim  # the stride of a single row carries no meaning
-    _need_flat(positions, "positions", torch.int32, dev, tokens)
-    _need_flat(slots, "slots", torch.int32, dev, tokens)
-    _need(rope, "rope", torch.float32, dev, 2)
-    if rope.shape[1] != ROPE_DIM or not rope.is_contiguous():
-        raise ValueError("rope must be contiguous [max_positions, 64]")
-    _launch(name, dev, events, rows.data_ptr(), stride, VALUE_DTYPES[rows.dtype], positions.data_ptr(),
-            slots.data_ptr(), rope.data_ptr(), rope.shape[0], int(bool(interleaved)), tokens, pages.shape[0],
-            pages.data_ptr(), *tail)
-
-
-def _need_pages(t, name, dtype, dev, width):
-    _need(t, name, dtype, dev, 3)
-    if t.shape[1] != PAGE_TOKENS or t.shape[2] != width or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [P, 64, {width}]")
+    _need_shaped(positions, "positions", torch.int32, dev, (tokens,))
+    _need_shaped(slots, "slots", torch.int32, dev, (tokens,))
+    max_positions = rope.shape[0]
+    _need_shaped(rope, "rope", torch.float32, dev, (max_positions, ROPE_DIM))
+    _launch(name, dev, events, rows.data_ptr(), stride, VALUE_DTYPES[dtype], positions.data_ptr(), slots.data_ptr(),
+            rope.data_ptr(), max_positions, 1 if interleaved else 0, tokens, pages.shape[0], pages.data_ptr(), *tail)
 
 
 def index_k_append(k, positions, slots, rope, kv_pages, k_scales, interleaved=False, events=None):
@@ -656,17 +657,16 @@ def index_k_append(k, positions, slots, rope, kv_pages, k_scales, interleaved=Fa
     64 dimensions are rotated in pairs (i, i + 32), or (2i, 2i + 1) with
     ``interleaved``.
     """
-    _need_pages(kv_pages, "kv_pages", torch.uint8, k.device, HEAD_DIM)
-    _need(k_scales, "k_scales", torch.float32, k.device, 2)
-    if tuple(k_scales.shape) != (kv_pages.shape[0], PAGE_TOKENS) or not k_scales.is_contiguous():
-        raise ValueError("k_scales must be contiguous [P, 64]")
+    dev, pages = k.device, kv_pages.shape[0]
+    _need_shaped(kv_pages, "kv_pages", torch.uint8, dev, (pages, PAGE_TOKENS, HEAD_DIM))
+    _need_shaped(k_scales, "k_scales", torch.float32, dev, (pages, PAGE_TOKENS))
     _append_call("index_k_append", HEAD_DIM, (torch.bfloat16, torch.float16, torch.float32), k, positions, slots,
                  rope, kv_pages, (_ptr(k_scales),), interleaved, events)
 
 
 def index_k_append_mxfp4(k, positions, slots, rope, kv_pages, interleaved=False, events=None):
     """index_k_append into packed MXFP4 tokens: kv_pages [P, 64, 68] uint8."""
-    _need_pages(kv_pages, "kv_pages", torch.uint8, k.device, MXFP4_TOKEN_BYTES)
+    _need_shaped(kv_pages, "kv_pages", torch.uint8, k.device, (kv_pages.shape[0], PAGE_TOKENS, MXFP4_TOKEN_BYTES))
     _append_call("index_k_append_mxfp4", HEAD_DIM, (torch.bfloat16, torch.float16, torch.float32), k, positions,
                  slots, rope, kv_pages, (), interleaved, events)
 
@@ -678,7 +678,7 @@ def latent_append(kv, positions, slots, rope, latent_pages, interleaved=False, e
     latent_pages [P, 64, 576] of the same type; positions, slots, rope and
     ``interleaved`` as for index_k_append; dimensions 512..575 are rotated.
     """
-    _need_pages(latent_pages, "latent_pages", kv.dtype, kv.device, LATENT_ROW)
+    _need_shaped(latent_pages, "latent_pages", kv.dtype, kv.device, (latent_pages.shape[0], PAGE_TOKENS, LATENT_ROW))
     _append_call("latent_append", LATENT_ROW, (torch.bfloat16, torch.float16), kv, positions, slots, rope,
                  latent_pages, (), interleaved, events)
 
@@ -695,51 +695,47 @@ def shared_prefix_workspace_bytes(rows: int, heads: int, requests: int) -> int:
 def _attention_call(name, q, latent_pages, block_table, keys, next_n, cu_q, starts, prefix_pages, scale, out, lse,
                     softcap, slopes, row_positions, workspace, events):
     """keys: row_lens [rows], or the selected keys [rows, k] (sparse_attention)."""
-    dev = q.device
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    _need(q, "q", q.dtype, dev, 3)
-    rows, heads, dim = q.shape
-    if dim != LATENT_ROW or not q.is_contiguous():
-        raise ValueError("q must be contiguous [rows, heads, 576]")
-    _need_pages(latent_pages, "latent_pages", q.dtype, dev, LATENT_ROW)
-    _rows2(block_table, "block_table", torch.int32, dev)
+    dev, dtype = q.device, q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+    rows, heads = q.shape[:2]
+    _need_shaped(q, "q", dtype, dev, (rows, heads, LATENT_ROW))
+    pages = latent_pages.shape[0]
+    _need_shaped(latent_pages, "latent_pages", dtype, dev, (pages, PAGE_TOKENS, LATENT_ROW))
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must have 2 dims, got {tuple(block_table.shape)}")
     requests, max_pages = block_table.shape
+    _need_shaped(block_table, "block_table", torch.int32, dev, (requests, max_pages))
     sparse = name == "sparse_attention"
     if sparse:
-        _need(keys, "indices", torch.int32, dev, 2)
-        if keys.shape[0] != rows or not keys.is_contiguous():
-            raise ValueError("indices must be contiguous [rows, k]")
+        _need_shaped(keys, "indices", torch.int32, dev, (rows, keys.shape[-1]))
     else:
-        _need_flat(keys, "row_lens", torch.int32, dev, rows)
+        _need_shaped(keys, "row_lens", torch.int32, dev, (rows,))
     if starts is not None:
-        _need_flat(starts, "row_starts", torch.int32, dev, rows)
+        _need_shaped(starts, "row_starts", torch.int32, dev, (rows,))
     if cu_q is not None:
-        _need_flat(cu_q, "cu_q", torch.int32, dev, requests + 1)
+        _need_shaped(cu_q, "cu_q", torch.int32, dev, (requests + 1,))
     if row_positions is not None:
-        _need_flat(row_positions, "row_positions", torch.int32, dev, rows)
+        _need_shaped(row_positions, "row_positions", torch.int32, dev, (rows,))
     if slopes is not None:
-        _need_flat(slopes, "slopes", torch.float32, dev, heads)
-    _need(out, "out", q.dtype, dev, 3)
-    if out.shape != (rows, heads, LATENT_DIM) or not out.is_contiguous():
-        raise ValueError(f"out must be contiguous [{rows}, {heads}, 512]")
+        _need_shaped(slopes, "slopes", torch.float32, dev, (heads,))
+    _need_shaped(out, "out", dtype, dev, (rows, heads, LATENT_DIM))
     if lse is not None:
-        _need(lse, "lse", torch.float32, dev, 2)
-        if lse.shape != (rows, heads) or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous [{rows}, {heads}]")
-    lib = load_library()
+        _need_shaped(lse, "lse", torch.float32, dev, (rows, heads))
     if workspace is None:
         # the caching allocator orders it with the stream, and inside a graph
         # capture it belongs to that graph
-        size = lib.shared_prefix_workspace_bytes if prefix_pages is not None else lib.attention_workspace_bytes
+        size = shared_prefix_workspace_bytes if prefix_pages is not None else attention_workspace_bytes
         workspace = torch.empty(size(rows, heads, requests), dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, dev)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    head = (q.data_ptr(), latent_pages.data_ptr(), VALUE_DTYPES[q.dtype], block_table.data_ptr(), keys.data_ptr())
+    head = (q.data_ptr(), latent_pages.data_ptr(), VALUE_DTYPES[dtype], block_table.data_ptr(), keys.data_ptr())
     shape = (rows, heads, requests, next_n)
-    tail = (latent_pages.shape[0], max_pages, scale, softcap, _ptr(slopes), _ptr(row_positions), out.data_ptr(),
+    tail = (pages, max_pages, scale, softcap, _ptr(slopes), _ptr(row_positions), out.data_ptr(),
             _ptr(lse), workspace.data_ptr(), workspace.numel())
     if sparse:
         _launch(name, dev, events, *head, keys.shape[1], _ptr(cu_q), *shape, *tail)

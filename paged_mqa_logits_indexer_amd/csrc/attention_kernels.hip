@@ -736,11 +736,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     const uint32_t q_ring = ring + kRingBytes - M * kRowBytes;
     const int64_t pair_base = static_cast<int64_t>(it.row0) * a.heads + it.pair0;  // over the whole batch
     lds_barrier();  // the previous item's epilogue has left the ring
-    for (int o = wave; o < M / 8; o += 4) {
-      const int pair = 8 * o + (lane >> 3);
-      const char* from = (pair < it.pairs ? static_cast<const char*>(a.q) + (pair_base + pair) * kRowBytes : zero) +
-                         (((lane & 7) ^ swz(pair & 15)) * 16);
-      load_octet(from, q_ring + o * kOctBytes);
+    if constexpr (KIND != kSparse) {  // asked for together with what the pairs need to know
+      page_window = (it.tile0 + lo) >> 6;
+      window_page = table[min(page_window * 64 + lane, a.max_pages - 1)];
     }
     for (int local = tid; local < M; local += kAttnThreads) {
       const int pair = it.pair0 + min(local, it.pairs - 1);
@@ -761,6 +759,13 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     if constexpr (KIND == kSparse) {
       resolve(step0 * S::kKeys / kWindow, std::integral_constant<int, kWindow / kAttnThreads>{});
       lds_barrier();
+    }
+    if constexpr (KIND != kSparse) __asm__ volatile("" : "+v"(window_page));
+    for (int o = wave; o < M / 8; o += 4) {
+      const int pair = 8 * o + (lane >> 3);
+      const char* from = (pair < it.pairs ? static_cast<const char*>(a.q) + (pair_base + pair) * kRowBytes : zero) +
+                         (((lane & 7) ^ swz(pair & 15)) * 16);
+      load_octet(from, q_ring + o * kOctBytes);
     }
     // narrow: slot 0 holds step0's keys, slot 1 the queries
     if constexpr (!S::kWide) issue(step0);
