@@ -86,6 +86,7 @@ typedef enum { IDX_BF16 = 0, IDX_FP16 = 1, IDX_FP32 = 2 } idx_value_dtype;
 #define IDX_MAX_ATTENTION_HEADS 128
 #define IDX_MAX_APPEND_TOKENS (1 << 24)
 #define IDX_MAX_CACHE_PAGES ((1 << 25) - 1) /* 64 * pages stays a 32-bit integer */
+#define IDX_MAX_ATTENTION_PAGES (1 << 20)   /* of one request: 67,108,864 keys */
 /* topk_rows_noalloc: rows its fixed scratch holds (chunked path only). */
 #define IDX_NOALLOC_MAX_ROWS 128
 
@@ -520,14 +521,15 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * block_table  (device) int32 [requests][max_pages]; ids clamped into the cache
  * requests     1 .. IDX_MAX_REQUESTS; rows 1 .. IDX_MAX_ROWS;
  *              heads 1 .. IDX_MAX_ATTENTION_HEADS;
- *              num_pages, max_pages 1 .. IDX_MAX_CACHE_PAGES, requests * max_pages < 2^31
+ *              num_pages 1 .. IDX_MAX_CACHE_PAGES; max_pages 1 ..
+ *              IDX_MAX_ATTENTION_PAGES, requests * max_pages < 2^31
  * next_n, cu_q next_n > 0 and cu_q NULL: rows = requests * next_n, row r
  *              belongs to request r / next_n.  next_n 0 and cu_q (device)
  *              int32 [requests + 1], ascending: request b owns rows cu_q[b] ..
  *              cu_q[b+1]-1; rows of no request are not written.
- * scale        finite; softcap finite, >= 0
+ * scale        finite; softcap finite, >= 0, and scale / softcap finite
  * slopes       (device) float [heads], or NULL: no distance bias
- * row_positions(device) int32 [rows], or NULL: row_lens - 1
+ * row_positions(device) int32 [rows] within +-2^30, or NULL: row_lens - 1
  * out          (device) [rows][heads][512] of q's type, 16-B aligned
  * lse          (device) float [rows][heads], or NULL
  * workspace    (device) scratch of at least attention_workspace_bytes(rows,

@@ -405,9 +405,10 @@ static idx_status check_attention(const pmqa::AttentionArgs& a, const void* keys
   if ((a.cu_q != nullptr) == (a.next_n > 0)) return IDX_EINVAL;
   if (!a.cu_q && static_cast<int64_t>(a.requests) * a.next_n != a.rows) return IDX_EINVAL;
   if (!std::isfinite(a.scale) || !std::isfinite(a.softcap) || a.softcap < 0.0f) return IDX_EINVAL;
+  if (a.softcap > 0.0f && !std::isfinite(a.scale / a.softcap)) return IDX_EINVAL;
   if (a.dtype != IDX_BF16 && a.dtype != IDX_FP16) return IDX_EUNSUPPORTED;
   if (a.rows > IDX_MAX_ROWS || a.heads > IDX_MAX_ATTENTION_HEADS || a.requests > IDX_MAX_REQUESTS ||
-      a.num_pages > IDX_MAX_CACHE_PAGES || a.max_pages > IDX_MAX_CACHE_PAGES ||
+      a.num_pages > IDX_MAX_CACHE_PAGES || a.max_pages > IDX_MAX_ATTENTION_PAGES ||
       static_cast<int64_t>(a.requests) * a.max_pages > INT32_MAX)
     return IDX_EUNSUPPORTED;
   if (!aligned(a.q, 16) || !aligned(a.cache, 16) || !aligned(a.block_table, 4) || !aligned(keys, 4) ||

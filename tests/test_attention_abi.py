@@ -84,11 +84,11 @@ def attend(lib, name, **kw):
     (dict(next_n=1 << 30, requests=4, rows=8), IDX_EINVAL),
     (dict(scale=float("nan")), IDX_EINVAL), (dict(scale=float("inf")), IDX_EINVAL),
     (dict(softcap=-1.0), IDX_EINVAL), (dict(softcap=float("inf")), IDX_EINVAL),
-    (dict(softcap=float("nan")), IDX_EINVAL),
+    (dict(softcap=float("nan")), IDX_EINVAL), (dict(scale=1e10, softcap=1e-30), IDX_EINVAL),
     (dict(dtype=FP32), IDX_EUNSUPPORTED), (dict(dtype=7), IDX_EUNSUPPORTED), (dict(heads=129), IDX_EUNSUPPORTED),
     (dict(rows=65536, requests=4096, next_n=16), IDX_EUNSUPPORTED),
     (dict(rows=8194, requests=4097), IDX_EUNSUPPORTED), (dict(pages=1 << 25), IDX_EUNSUPPORTED),
-    (dict(max_pages=1 << 25), IDX_EUNSUPPORTED),
+    (dict(max_pages=(1 << 20) + 1), IDX_EUNSUPPORTED),
     (dict(rows=8192, requests=4096, max_pages=1 << 20), IDX_EUNSUPPORTED),
     (dict(q=A + 8), IDX_EALIGN), (dict(cache=A + 8), IDX_EALIGN), (dict(bt=A + 2), IDX_EALIGN),
     (dict(lens=A + 2, idx=A + 2), IDX_EALIGN), (dict(out=A + 8), IDX_EALIGN), (dict(lse=A + 2), IDX_EALIGN),

@@ -20,9 +20,12 @@ SCALE = 192 ** -0.5
 
 class Batch:
     """Rows over requests' pages.  rows: rows of each request; ends: keys of
-    each row; starts: first key of each row (or None)."""
+    each row; starts: first key of each row (or None); width: columns of the
+    block table (the calls size their pair tiles by it: with WIDE columns 33 to
+    64 pairs together take 64-pair tiles and more of them 128-pair tiles, with
+    the few that the lengths need 16- and 32-pair tiles)."""
 
-    def __init__(self, seed, heads, rows, ends, starts=None, dtype="bf16", shared=0, spare=3, q_scale=1.0):
+    def __init__(self, seed, heads, rows, ends, starts=None, dtype="bf16", shared=0, spare=3, q_scale=1.0, width=0):
         rng = np.random.default_rng(seed)
         self.rng, self.heads, self.dtype = rng, heads, dtype
         self.counts = list(rows)
@@ -32,7 +35,7 @@ class Batch:
         assert len(self.ends) == self.first[-1]
         need = [max([1] + [-(-int(e) // 64) for e in self.ends[a:b]]) for a, b in zip(self.first[:-1], self.first[1:])]
         need = [max(n, shared) for n in need]
-        self.max_pages = max(need)
+        self.max_pages = max(max(need), width)
         self.pages = sum(n - shared for n in need) + shared + spare
         perm = rng.permutation(self.pages)
         self.table = rng.integers(-5, self.pages + 5, (len(need), self.max_pages)).astype(np.int32)
@@ -99,33 +102,66 @@ class Batch:
             assert (np.abs(lse[r] - wl) <= lb).all(), f"row {r} lse: {np.abs(lse[r] - wl).max()} over {lb.min()}"
 
 
+WIDE = 1200
+WIDTHS = pytest.mark.parametrize("width", [0, WIDE])
 LENGTHS = [1, 63, 64, 65, 0, 127, 128, 200, 2, 333]
 
 
+@WIDTHS
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("heads,next_n", [(1, 1), (3, 1), (16, 1), (17, 1), (16, 2), (32, 1), (24, 3), (64, 1),
                                           (100, 1), (128, 1), (128, 2)])
-def test_paged_decode(gpu, heads, next_n, dtype):
+def test_paged_decode(gpu, heads, next_n, dtype, width):
     """Head counts that fill pair tiles and ones that do not, lengths around
     page ends, verify rows (row j sees L + j keys), an empty request."""
     announce(f"paged_attention heads={heads} next_n={next_n} {dtype}")
     ends = [n + j if n else 0 for n in LENGTHS for j in range(next_n)]
-    b = Batch(100 + heads + next_n, heads, [next_n] * len(LENGTHS), ends, dtype=dtype)
+    b = Batch(100 + heads + next_n, heads, [next_n] * len(LENGTHS), ends, dtype=dtype, width=width)
     b.check(*b.run(gpu))
 
 
+@WIDTHS
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("heads", [8, 16, 128])
-def test_paged_long(gpu, heads, dtype):
+def test_paged_long(gpu, heads, dtype, width):
     """Requests that many workgroups share, beside short ones."""
     announce(f"paged_attention long heads={heads} {dtype}")
-    b = Batch(7, heads, [1] * 4, [9001, 5, 0, 4097], dtype=dtype, q_scale=2.0)
+    b = Batch(7, heads, [1] * 4, [9001, 5, 0, 4097], dtype=dtype, q_scale=2.0, width=2 * width)
     b.check(*b.run(gpu))
 
 
+def growing(b, seed):
+    """Keys whose scores grow along the request, by far more than 2^60 in the
+    weights: every running maximum is passed many times."""
+    flat = b.cache.view(-1, 576).float()
+    for r in range(len(b.ends)):
+        at = np.arange(int(b.ends[r]))
+        # (requests without pages in common)
+        flat[torch.from_numpy(b.slots(r, at))] *= torch.from_numpy(0.05 + 8.0 * at / max(1, len(at)))[:, None].float()
+    b.cache = flat.to(b.cache.dtype).view(b.cache.shape)
+
+
+@WIDTHS
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+def test_growing_scores(gpu, heads, dtype, width):
+    announce(f"paged and sparse attention growing scores heads={heads} {dtype}")
+    b = Batch(37, heads, [1] * 5, [3000, 900, 400, 64, 2100], dtype=dtype, q_scale=4.0, width=width)
+    growing(b, 1)
+    b.check(*b.run(gpu))
+    lists = np.full((5, 3000), -1, np.int32)
+    for r, n in enumerate(b.ends):
+        lists[r, :n] = np.arange(n)
+    out, lse = b.out()
+    gpu.sparse_attention(b.q.to(DEV), b.cache.to(DEV), b.dev(b.table), b.dev(lists), 1, SCALE, out, lse)
+    torch.cuda.synchronize()
+    b.check(out, lse)
+
+
+@WIDTHS
 @pytest.mark.parametrize("mask", ["causal", "window", "document", "prefix", "empty"])
 @pytest.mark.parametrize("heads", [4, 16, 48])
-def test_paged_ragged_masks(gpu, heads, mask):
+def test_paged_ragged_masks(gpu, heads, mask, width):
     """Ragged extend batches: pair tiles hold several rows with key ranges of
     their own; requests without rows; rows whose range is empty."""
     announce(f"paged_attention ragged {mask} heads={heads}")
@@ -141,21 +177,22 @@ def test_paged_ragged_masks(gpu, heads, mask):
         ends = np.minimum(np.maximum(ends, 100), total)
     elif mask == "empty":
         starts = np.where(np.arange(len(pos)) % 3 == 0, ends + np.arange(len(pos)) % 5, np.maximum(0, ends - 70))
-    b = Batch(31, heads, rows, ends, starts)
+    b = Batch(31, heads, rows, ends, starts, width=width)
     b.check(*b.run(gpu))
 
 
+@WIDTHS
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("softcap,bias,given", [(20.0, False, False), (0.0, True, False), (30.0, True, True),
                                                 (0.5, True, True)])
-def test_paged_scores(gpu, softcap, bias, given, dtype):
+def test_paged_scores(gpu, softcap, bias, given, dtype, width):
     """Capped scores and the distance bias, on keys before and after the row."""
     announce(f"paged_attention softcap={softcap} bias={bias} {dtype}")
     heads, rows, prefix = 16, [9, 30, 2], [0, 300, 70]
     pos = np.concatenate([np.arange(p, p + n) for n, p in zip(rows, prefix)])
     total = np.repeat([p + n for n, p in zip(rows, prefix)], rows)
     ends = np.minimum(pos + 12, total) if given else pos + 1
-    b = Batch(41, heads, rows, ends, dtype=dtype, q_scale=3.0)
+    b = Batch(41, heads, rows, ends, dtype=dtype, q_scale=3.0, width=width)
     slopes = (2.0 ** (-8.0 * np.arange(1, heads + 1) / heads)).astype(np.float32) if bias else None
     positions = pos.astype(np.int32) if given else None
     out, lse = b.run(gpu, softcap=softcap, slopes=b.dev(slopes), row_positions=b.dev(positions))
@@ -185,13 +222,15 @@ def test_rows_behind_the_batch_stay(gpu):
     assert (out[11:] == 5).all() and (lse[11:] == 5).all()
 
 
+@WIDTHS
+@pytest.mark.parametrize("heads", [4, 16])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_hidden_nan_next_to_rows_that_see_it(gpu, dtype):
+def test_hidden_nan_next_to_rows_that_see_it(gpu, dtype, heads, width):
     """Keys with NaN and infinities that some rows of a pair tile see and
     others do not: the others stay clean, the ones that see a NaN are NaN."""
     announce(f"paged_attention hidden NaN {dtype}")
     ends = np.arange(90, 98)
-    b = Batch(61, 4, [8], ends, dtype=dtype)
+    b = Batch(61, heads, [8], ends, dtype=dtype, width=8 * width)
     flat = b.cache.view(-1, 576)
     slot = b.slots(0, np.arange(98))
     flat[slot[93], 7] = float("nan")     # seen by rows with end >= 94
@@ -202,10 +241,11 @@ def test_hidden_nan_next_to_rows_that_see_it(gpu, dtype):
     assert torch.isnan(out[4:]).all() and torch.isnan(lse[4:]).all()
 
 
+@WIDTHS
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("heads,requests,next_n,prefix", [(16, 5, 1, 1), (16, 9, 2, 4), (128, 3, 1, 7), (5, 33, 1, 2),
                                                           (40, 2, 4, 40)])
-def test_shared_prefix(gpu, heads, requests, next_n, prefix, dtype):
+def test_shared_prefix(gpu, heads, requests, next_n, prefix, dtype, width):
     """Requests with tails of none, one and many keys behind the prefix, one
     that ends inside it, and an empty one."""
     announce(f"shared_prefix_attention heads={heads} requests={requests} prefix={prefix} {dtype}")
@@ -214,7 +254,7 @@ def test_shared_prefix(gpu, heads, requests, next_n, prefix, dtype):
     ends[:next_n] = prefix * 64 - 30
     if requests > 3:
         ends[2 * next_n:3 * next_n] = 0
-    b = Batch(71, heads, [next_n] * requests, ends, shared=prefix, dtype=dtype)
+    b = Batch(71, heads, [next_n] * requests, ends, shared=prefix, dtype=dtype, width=width)
     out, lse = b.out()
     gpu.shared_prefix_attention(b.q.to(DEV), b.cache.to(DEV), b.dev(b.table), b.dev(b.ends.astype(np.int32)), next_n,
                                 prefix, SCALE, out, lse)
@@ -222,14 +262,15 @@ def test_shared_prefix(gpu, heads, requests, next_n, prefix, dtype):
     b.check(out, lse)
 
 
-def test_shared_prefix_masks_and_scores(gpu):
+@WIDTHS
+def test_shared_prefix_masks_and_scores(gpu, width):
     """Windows that begin inside, at the end of and behind the prefix; caps and
     slopes; a table that holds nothing but the prefix."""
     announce("shared_prefix_attention masks")
     heads, prefix = 16, 3
     ends = np.array([250, 260, 200, 192, 300, 193])
     starts = np.array([100, 192, 195, 0, 299, 64])
-    b = Batch(81, heads, [1] * 6, ends, starts, shared=prefix)
+    b = Batch(81, heads, [1] * 6, ends, starts, shared=prefix, width=width)
     slopes = np.linspace(0.01, 0.5, heads).astype(np.float32)
     pos = (ends + 3).astype(np.int32)
     out, lse = b.out()
@@ -273,6 +314,51 @@ def test_sparse(gpu, heads, k, dtype):
     gpu.sparse_attention(b.q.to(DEV), b.cache.to(DEV), b.dev(b.table), b.dev(lists), 1, SCALE, out, lse)
     torch.cuda.synchronize()
     b.check(out, lse, picked=picked)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,rows", [(128, 24), (50, 40)])
+@pytest.mark.parametrize("scores", [False, True])
+def test_sparse_large_tiles(gpu, heads, rows, scores, dtype):
+    """Selections that take 128- and 64-pair tiles: long lists, mostly padding,
+    whole steps of it among them; with caps and slopes, too."""
+    announce(f"sparse_attention large tiles heads={heads} {dtype} scores={scores}")
+    k = 8192
+    b = Batch(99, heads, [rows], np.arange(rows) * 31 + 200, dtype=dtype, q_scale=2.0)
+    rng = np.random.default_rng(8)
+    lists = np.full((rows, k), -1, np.int32)
+    picked = []
+    for r, end in enumerate(b.ends):
+        n = 0 if r == 3 else rng.integers(1, min(int(end), 400) + 1)
+        chosen = rng.permutation(int(end))[:n]
+        first = rng.integers(0, 7000)
+        lists[r, np.sort(first + rng.permutation(1100)[:n])] = chosen
+        picked.append(chosen)
+    slopes = np.linspace(0.01, 0.5, heads).astype(np.float32) if scores else None
+    pos = (b.ends + 5).astype(np.int32) if scores else None
+    cap = 20.0 if scores else 0.0
+    out, lse = b.out()
+    gpu.sparse_attention(b.q.to(DEV), b.cache.to(DEV), b.dev(b.table), b.dev(lists), rows, SCALE, out, lse,
+                         softcap=cap, slopes=b.dev(slopes), row_positions=b.dev(pos))
+    torch.cuda.synchronize()
+    b.check(out, lse, cap, slopes, pos, picked=picked)
+
+
+@pytest.mark.parametrize("heads,rows", [(16, 2), (40, 2), (128, 2), (128, 300)])
+def test_sparse_long_lists(gpu, heads, rows):
+    """Lists longer than the keys that are resolved at a time, for few rows
+    (cut into parts) and for many (whole rows)."""
+    announce(f"sparse_attention long lists heads={heads} rows={rows}")
+    b = Batch(97, heads, [rows], [6000 - r for r in range(rows)])
+    rng = np.random.default_rng(3)
+    lists = np.stack([rng.permutation(5600)[:5000] for _ in range(rows)]).astype(np.int32)
+    lists[rng.random(lists.shape) < 0.05] = -1
+    picked = [row[row >= 0] for row in lists]
+    out, lse = b.out()
+    gpu.sparse_attention(b.q.to(DEV), b.cache.to(DEV), b.dev(b.table), b.dev(lists), rows, SCALE, out, lse)
+    torch.cuda.synchronize()
+    b.check(out, lse, picked=picked, rows=range(rows) if rows < 10 else [0, 1, 77, 255, 256, 299])
+    assert torch.isfinite(out).all()
 
 
 @pytest.mark.parametrize("ragged", [False, True])
