@@ -21,7 +21,8 @@
 //
 // Every lane moves 16-byte pieces and no lane waits for another token's, so
 // the kernels are bound by memory (and, for a few tokens, by one dependent
-// load chain: slot and position, then the table row).
+// load chain: slot and position, then the table row).  Measured: 8192 latent
+// rows 6.1 us (21 MB, 3.4 TB/s), 8191 MXFP4 keys 3.9 us, 8 FP8 keys 2.1 us.
 #include "indexer_common.h"
 #include "launches.h"
 

@@ -22,6 +22,13 @@
 // output; the pieces of a pair tile that several workgroups share go to the
 // workspace as (o, m, l) in float32 and a second kernel joins them, in a fixed
 // order.
+//
+// Measured (MI355X, kernel alone): 64 requests of 1 .. 32768 keys with 16 heads
+// 47 us (a K stream of 240 MB in about 35 us, the rest each workgroup's start
+// and end); 1024 rows of 128 heads over 2048 selected keys 611 us (625 TFLOP/s;
+// the library's 8192^3 product reaches 1193), the MFMAs busy 43 % of all cycles
+// and 55 - 60 % within a step; 8 requests on 32768 shared keys 92 us; one
+// request of 65 keys 9.3 us, five dependent round trips to memory.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
