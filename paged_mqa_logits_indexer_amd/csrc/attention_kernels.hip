@@ -911,9 +911,10 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         constexpr int kReads = kKSteps * ST, kRing = 8;
         f32x4 s[ST][kChains] = {};
         s16x8 kk[kRing];
+        const uint32_t at[2] = {opaque(base + k_at), opaque(base + (k_at ^ 64))};
         auto read = [&](int r) {
           const int ks = r / ST, st = r % ST;
-          kk[r % kRing] = lds_read(base + (k_at ^ ((ks & 1) * 64)) + st * kBlkBytes + (ks >> 1) * 1024);
+          kk[r % kRing] = lds_read(at[ks & 1] + st * kBlkBytes + (ks >> 1) * 1024);
         };
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -1058,10 +1059,13 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         if constexpr (!S::kWide) {
           constexpr int kRing = ST == 1 ? 10 : ST == 2 ? 6 : 4;
           s16x4 v[kRing][ST];
+          uint32_t at[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at[i] = opaque(base + (v_at ^ (i * 32)));
           auto read = [&](int d) {
 #pragma unroll
             for (int st = 0; st < ST; ++st)
-              v[d % kRing][st] = lds_read_tr(base + (v_at ^ ((d & 3) * 32)) + (d >> 2) * 1024 + st * kBlkBytes);
+              v[d % kRing][st] = lds_read_tr(at[d & 3] + (d >> 2) * 1024 + st * kBlkBytes);
           };
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
