@@ -513,8 +513,10 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * block_table[request][s / 64].  Products and the softmax are summed in
  * float32; the softmax weights are rounded to the cache's type for the product
  * with the values.  What the cache holds at keys a row does not see, NaN and
- * infinities included, does not reach that row.  A row that sees a NaN, or
- * whose score is +infinity, is NaN.
+ * infinities included, does not reach that row.  A row that sees a NaN, whose
+ * scale * q . k_s is +infinity, or -infinity under a softcap, is NaN.  Without
+ * a softcap a score of -infinity has the weight zero, and outputs at which such
+ * a key's value is infinite may be NaN.
  *
  * q            (device) [rows][heads][576], dtype BF16 or FP16, 16-B aligned
  * latent_pages (device) [num_pages][64][576] of the same type, 16-B aligned

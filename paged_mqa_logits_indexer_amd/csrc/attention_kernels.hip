@@ -946,8 +946,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       const int step_key = step * S::kKeys;  // of the item's list
       if (a.softcap > 0.0f) {
         const float in = a.scale / a.softcap, cap = a.softcap * kLog2e;
+        // (z - z: 0, and NaN where z is not finite, which tanh would hide)
 #pragma unroll
-        for (int i = 0; i < kScores; ++i) z[i] = cap * tanh_f32(z[i] * in);
+        for (int i = 0; i < kScores; ++i) z[i] = __builtin_fmaf(cap, tanh_f32(z[i] * in), z[i] - z[i]);
       } else if (!S::kWide || prescale) {
 #pragma unroll
         for (int i = 0; i < kScores; ++i) z[i] *= to_log2;
@@ -995,7 +996,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
 
       // A key that some rows of the pair tile see and others do not may hold an
       // infinity or a NaN; a weight of zero would not take it out of the
-      // product.  Rows that see it get their NaN from S.
+      // product.  Rows that see it get their NaN from S, also under a cap; a
+      // score of -inf leaves the key a weight of zero.
       auto clear_nonfinite = [&] {
         __syncthreads();
         for (int i = tid; i < S::kSlotBytes / 16; i += kAttnThreads) {

@@ -243,6 +243,23 @@ def test_hidden_nan_next_to_rows_that_see_it(gpu, dtype, heads, width):
 
 @WIDTHS
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [200, 560])
+def test_infinity_under_a_cap(gpu, dtype, dim, width):
+    """A capped score is finite, also that of a key with an infinity: the rows
+    that see the key are NaN all the same, whichever part of a key holds it and
+    whether or not other rows of the pair tile see the key too."""
+    announce(f"paged_attention capped infinity {dtype} dim {dim}")
+    for ends in (np.arange(90, 98), np.arange(120, 128)):
+        b = Batch(63, 16, [8], ends, dtype=dtype, width=8 * width)
+        b.cache.view(-1, 576)[b.slots(0, np.array([96]))[0], dim] = float("inf")
+        out, lse = b.run(gpu, softcap=20.0)
+        seen = ends > 96
+        b.check(out, lse, softcap=20.0, rows=np.flatnonzero(~seen))
+        assert torch.isnan(out[seen]).all() and torch.isnan(lse[seen]).all()
+
+
+@WIDTHS
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("heads,requests,next_n,prefix", [(16, 5, 1, 1), (16, 9, 2, 4), (128, 3, 1, 7), (5, 33, 1, 2),
                                                           (40, 2, 4, 40)])
 def test_shared_prefix(gpu, heads, requests, next_n, prefix, dtype, width):
