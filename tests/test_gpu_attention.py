@@ -493,6 +493,31 @@ def test_graphs_share_a_workspace(gpu):
                     assert torch.equal(x, y), f"eager {turn}"
 
 
+def test_two_streams_at_once(gpu):
+    """Calls on two streams in flight together, each with the workspace that the
+    call takes for itself, give the bits of calls alone."""
+    announce("attention on two streams")
+    batches = [Batch(131 + i, 16 + 112 * i, [1] * 6, [1500, 30, 700, 2500, 129, 64], shared=0) for i in range(2)]
+    runs = []
+    for b in batches:
+        lists, _ = selections(b, 300, 9)
+        args = [b.q.to(DEV), b.cache.to(DEV), b.dev(b.table), b.dev(b.ends.astype(np.int32)), b.dev(lists)]
+        alone = [b.out() for _ in range(2)]
+        gpu.paged_attention(*args[:4], 1, SCALE, *alone[0])
+        gpu.sparse_attention(*args[:3], args[4], 1, SCALE, *alone[1])
+        runs.append((args, alone, [b.out() for _ in range(2)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for args, _, outs, stream in runs:
+            with torch.cuda.stream(stream):
+                gpu.paged_attention(*args[:4], 1, SCALE, *outs[0])
+                gpu.sparse_attention(*args[:3], args[4], 1, SCALE, *outs[1])
+    torch.cuda.synchronize()
+    for _, alone, outs, _ in runs:
+        for want, got in zip(alone, outs):
+            assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 def test_forms_agree(gpu):
     """The three operators on the same keys agree within the sum of their
     bounds, a call without lse or workspace gives the same bits, and two calls
