@@ -436,7 +436,8 @@ constexpr int kItemCost = M == 128 ? 6 : 3;
 template <int M>
 __device__ __forceinline__ int item_units(const Item& it) { return it.tiles ? it.tiles + kItemCost<M> : 0; }
 
-// Share of workgroup w: as many groups as give each min_units.
+// Share of workgroup w of a grid: equal parts [w, w + 1) / groups of the units,
+// of as many groups as have min_units each.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int groups, int w) {
   return total * w / groups;
 }
@@ -533,7 +534,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
 // What the join kernel needs to know of a pair tile that several workgroups
 // share: written by the workgroup that holds the tile's beginning.
 struct alignas(16) JoinInfo {
-  int first;      // first piece of the list (see piece_id)
+  int first;      // the first workgroup with a part of it
   int pieces;     // 0: nothing to join here
   int pairs;
   int pad;
@@ -552,8 +553,10 @@ __host__ __device__ __forceinline__ int64_t piece_floats(int m) { return static_
 // where fewer than four waves cover the pairs the others take other keys of
 // the same pairs (streams, joined at the end); their time is the K stream's.
 // Wide (M = 128): 32 pairs per wave, so that each LDS operand feeds twice the
-// arithmetic, and 32 keys per step in 4 slots: the value product of a step
-// runs while the next step's softmax is computed, two steps of loads ahead.
+// arithmetic, and 32 keys per step in 4 slots: the value product of a step runs
+// after the next step's scores, between whose MFMAs its weights are computed,
+// and two steps of loads are ahead.  (1024 rows of 128 heads over 2048 selected
+// keys, calls in a row: 624 us, with 64-pair tiles of the narrow form 793.)
 template <int M>
 struct Shape {
   static constexpr bool kWide = M == 128;
