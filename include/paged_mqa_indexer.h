@@ -512,7 +512,9 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * lse = -infinity.  Key s of a request is slot s % 64 of page
  * block_table[request][s / 64].  Products and the softmax are summed in
  * float32; the softmax weights are rounded to the cache's type for the product
- * with the values.  What the cache holds at keys a row does not see, NaN and
+ * with the values.  The sum is divided at its end: a row is finite as long as
+ * the magnitudes of its finite keys' values add up to less than 2^127 (always,
+ * in FP16).  What the cache holds at keys a row does not see, NaN and
  * infinities included, does not reach that row.  A row that sees a NaN, whose
  * scale * q . k_s is +infinity, or -infinity under a softcap, is NaN.  Without
  * a softcap a score of -infinity has the weight zero, and outputs at which such

@@ -70,17 +70,21 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // per key, independent over the keys, so it stays below the rounding of the
 // output itself; l sums the unrounded values.
 //
-// The running maximum is raised only when a score passes it by more than
-// kRaise (powers of two): until then P holds values above 1, exact in the final
-// quotient, and the accumulators need not be rescaled.  BF16 and float32 have
-// exponents for 2^60 (and 2^60 times a sum of 2^31 keys), so there a second
-// maximum hardly ever comes up.  FP16 ends at 2^16; its P is scaled by 2^8
-// (kShift), so that weights down to 2^-22 of the maximum are still normal.
+// The running maximum m is raised only when a score passes it by enough, so that
+// the accumulators are hardly ever rescaled: a first score z sets m = z - kShift,
+// and a later one is let pass until it is kRaise above z (powers of two).
+// BF16 has float32's exponents: with m 16 above the first score, P lies between
+// 2^-16 and 1 at the row's maximum, so an accumulator never passes the sum of
+// its values' magnitudes (a score let pass by 2^60 instead, with m at the first
+// score, turned values above 2^68 into infinities; neither measures faster), and
+// products of values down to 2^-110 are still normal.  FP16 ends at 2^16: m is 8
+// below the first score, so that weights down to 2^-22 of the maximum are still
+// normal, and P ends at 2^14.
 template <int DT>
 struct Elem;
 template <>
 struct Elem<IDX_BF16> {
-  static constexpr float kShift = 0.0f, kRaise = 60.0f;
+  static constexpr float kShift = -16.0f, kRaise = 16.0f;
   static __device__ __forceinline__ f32x4 mfma32(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);

@@ -1,0 +1,72 @@
+"""Attention over the latent cache where float32 comes near its ends: large and
+small values under scores that rise along a request, one key that outweighs the
+rest, and scores next to the lowest float32.  Scores are set through one rotated
+dimension, values through the latent ones."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from tests.gpu_harness import DEV, announce
+from tests.test_gpu_attention import DTYPES, SCALE, WIDE, Batch
+
+pytestmark = pytest.mark.gpu
+L = O.latent
+# heads and table width: between them all four sizes of pair tiles
+TILES = pytest.mark.parametrize("heads,width", [(16, 0), (32, WIDE), (64, WIDE), (128, WIDE)])
+FORMS = pytest.mark.parametrize("form", ["paged", "shared", "sparse"])
+
+
+def scored(seed, heads, lens, score, value, dtype="bf16", width=0, shared=0):
+    """A batch of one-row requests whose key s of request r has the score
+    (1 + h / 1024) * score(r, s) under head h, up to the rounding of the key, and
+    whose values are value(r, s) times numbers in +-[1, 2)."""
+    b = Batch(seed, heads, [1] * len(lens), lens, dtype=dtype, width=width, shared=shared)
+    t = DTYPES[dtype]
+    flat = b.cache.view(-1, 576)
+    rng = np.random.default_rng(seed)
+    for r, n in enumerate(lens):
+        at = np.arange(shared * 64 if r else 0, n)
+        rows = np.zeros((len(at), 576))
+        rows[:, :512] = (rng.choice([-1.0, 1.0], (len(at), 512)) * rng.uniform(1, 2, (len(at), 512)) *
+                         np.array([value(r, s) for s in at])[:, None])
+        rows[:, 512] = [score(r, s) for s in at]
+        flat[torch.from_numpy(b.slots(r, at))] = torch.from_numpy(rows).to(t)
+    b.q = torch.zeros(len(lens), heads, 576, dtype=t)
+    b.q[:, :, 512] = torch.tensor([(1 + h / 1024) / SCALE for h in range(heads)]).to(t)
+    return b
+
+
+def call(gpu, b, form, prefix=0, **kw):
+    """One call of the given form on all keys of the batch's rows."""
+    out, lse = b.out()
+    head = (b.q.to(DEV), b.cache.to(DEV), b.dev(b.table))
+    ends = b.dev(b.ends.astype(np.int32))
+    if form == "paged":
+        gpu.paged_attention(*head, ends, 1, SCALE, out, lse, **kw)
+    elif form == "shared":
+        gpu.shared_prefix_attention(*head, ends, 1, prefix, SCALE, out, lse, **kw)
+    else:
+        k = -(-int(b.ends.max()) // 64) * 64
+        lists = np.full((len(b.ends), k), -1, np.int32)
+        for r, n in enumerate(b.ends):
+            lists[r, :n] = np.arange(n)
+        gpu.sparse_attention(*head, b.dev(lists), 1, SCALE, out, lse, **kw)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@FORMS
+@TILES
+@pytest.mark.parametrize("size", [1e-30, 1.0, 1e22, 1e30, 1e35])
+def test_values_of_any_size(gpu, heads, width, size, form):
+    """Values times keys that end well inside float32 come out, however far a
+    later score rises over the first ones."""
+    announce(f"{form} attention heads={heads} width={width} values of {size}")
+    rises = [0.0, 3.3, 14.6, 17.1, 31.7, 58.9, 70.2, 120.4]  # powers of two
+    lens = [200 + 3 * r for r in range(len(rises))]
+    b = scored(201, heads, lens, lambda r, s: rises[r] * np.log(2) if s >= 150 else 0.0, lambda r, s: size,
+               width=width, shared=1)
+    out, lse = call(gpu, b, form, 1)
+    assert torch.isfinite(out).all()
+    b.check(out, lse)
