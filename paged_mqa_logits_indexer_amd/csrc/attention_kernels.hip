@@ -66,9 +66,14 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // P is rounded to the cache's 16-bit type for the second product (an MFMA
-// takes both operands in one type): a relative error of at most half a step
-// per key, independent over the keys, so it stays below the rounding of the
-// output itself; l sums the unrounded values.
+// takes both operands in one type), by at most half a step d_s of it per key.
+// The output is divided by the sum of the same rounded weights (one instruction
+// adds two of them to it in float32, to 1.5 steps and with FP16 subnormals, as
+// measured on a million of each type), so it is off by
+// sum p_s d_s (v_s - out): what all keys' weights have in common cancels, and
+// where one key outweighs the rest nothing is left (divided by the unrounded
+// sum, such a row is off by up to half a step as a whole).  The log of the sum,
+// and the shares of a pair's pieces, take the unrounded sum l.
 //
 // The running maximum m is raised only when a score passes it by enough, so that
 // the accumulators are hardly ever rescaled: a first score z sets m = z - kShift,
@@ -101,11 +106,11 @@ struct Elem<IDX_BF16> {
   static __device__ __forceinline__ f32x4 mfma16(s16x4 a, s16x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ short round(float x) {
-    return __builtin_bit_cast(short, static_cast<__bf16>(x));
-  }
   static __device__ __forceinline__ int round2(float x, float y) {
     return __builtin_bit_cast(int, __builtin_convertvector((f32x2{x, y}), bf16x2));
+  }
+  static __device__ __forceinline__ float add2(int both, float sum) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, both), bf16x2{1, 1}, sum, false);
   }
 };
 template <>
@@ -128,11 +133,11 @@ struct Elem<IDX_FP16> {
     return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
                                                  0);
   }
-  static __device__ __forceinline__ short round(float x) {
-    return __builtin_bit_cast(short, static_cast<_Float16>(x));
-  }
   static __device__ __forceinline__ int round2(float x, float y) {
     return __builtin_bit_cast(int, __builtin_convertvector((f32x2{x, y}), f16x2));
+  }
+  static __device__ __forceinline__ float add2(int both, float sum) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, both), f16x2{1, 1}, sum, false);
   }
 };
 
@@ -785,10 +790,16 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     if constexpr (!S::kWide) issue(step0);
     wait_and_barrier<0>();
     s16x8 q[kQ];
+    // wide: recomputed for every item (as 36 addresses kept over the items they go
+    // to scratch memory, one reload behind the other: 4 % of the call at 1024 rows
+    // as above)
+    uint32_t q_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q_at[i] = opaque(q_ring + pg * 32 * kRowBytes + (k_at ^ (i * 32)));
 #pragma unroll
     for (int ks = 0; ks < kQ; ++ks) {
       if constexpr (S::kWide)
-        q[ks] = lds_read(q_ring + pg * 32 * kRowBytes + (k_at ^ ((ks & 3) * 32)) + (ks >> 2) * 1024);
+        q[ks] = lds_read(q_at[ks & 3] + (ks >> 2) * 1024);
       else
         q[ks] = lds_read(q_ring + pg * 16 * kRowBytes + (k_at ^ ((ks & 1) * 64)) + (ks >> 1) * 1024);
     }
@@ -805,7 +816,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     Acc acc[kAccs];
 #pragma unroll
     for (int d = 0; d < kAccs; ++d) acc[d] = Acc{};
-    float m = kMInit, l = 0.0f;
+    float m = kMInit, l = 0.0f, l_kept = 0.0f;  // l_kept: of the rounded weights
     // wide: scores of the step before (of none before the first: weights of zero)
     // and its weights
     float z_before[kScores];
@@ -819,6 +830,13 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       int both = E::round2(e0, e1);
       __asm__ volatile("" : "+v"(both), "+v"(sum));  // computed here, between the MFMAs, and not where it is used
       p_wide[i / 4][i % 4] = both;
+    };
+
+    // (wide) the rounded weights into their sum, in the eight dimension tiles of
+    // the value product that no maximum is taken in
+    auto keep = [&](int i, float& kept) {
+      kept = E::add2(p_wide[i / 4][i % 4], kept);
+      __asm__ volatile("" : "+v"(kept));
     };
 
     // the value product of one step (wide), V^T P^T on the keys at `base`; each
@@ -1026,9 +1044,12 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         // its MFMAs; then the accumulators take it.  (The first step has none
         // before it: weights of zero on its own keys, which every row of the
         // pair tile sees or whose non-finite values have been cleared.)
-        float mx = -__builtin_inff();
+        float mx = -__builtin_inff(), kept = 0.0f;
         value_wide(step > step0 ? ring + ((step - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes : base, [&](int d) {
-          if (d < 8) mx = fmaxf(mx, fmaxf(z[2 * d], z[2 * d + 1]));
+          if (d < 8)
+            mx = fmaxf(mx, fmaxf(z[2 * d], z[2 * d + 1]));
+          else
+            keep(d - 8, kept);
         });
         mx = pair_max<true>(mx) * z_scale - E::kShift;
         const float raised = mx > m + E::kRaise ? mx : m;
@@ -1036,6 +1057,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         by = __builtin_amdgcn_exp2f(m - raised);
         m = raised;
         l *= by;
+        l_kept = (l_kept + kept) * by;
 #pragma unroll
         for (int i = 0; i < kScores; ++i) z_before[i] = z[i];
         return any_raised;
@@ -1051,6 +1073,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         m = raised;
         if (any_raised) {
           l *= by;
+          l_kept *= by;
 #pragma unroll
           for (int d = 0; d < kAccs; ++d) acc[d] *= by;
         }
@@ -1061,8 +1084,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
 #pragma unroll
           for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f(z[st * 4 + i] - m);
           l += (e[0] + e[1]) + (e[2] + e[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[st][i] = E::round(e[i]);
+          const int2 both = make_int2(E::round2(e[0], e[1]), E::round2(e[2], e[3]));
+          l_kept += E::add2(both.x, E::add2(both.y, 0.0f));
+          p[st] = __builtin_bit_cast(s16x4, both);
         }
         // ---- O^T += V^T P^T
         if constexpr (!S::kWide) {
@@ -1123,20 +1147,22 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       }
 #pragma unroll
       for (int d = 0; d < kAccs; ++d) pin(acc[d]);
-      float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) weigh(i, sum);
-      l += sum;
-      value_wide(ring + ((step_end - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes, [](int) {});
+      for (int i = 0; i < 8; ++i) weigh(i, l);
+      value_wide(ring + ((step_end - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes, [&](int d) {
+        if (d < 8) keep(d, l_kept);
+      });
     } else {
       for (int step = step0; step < step_end; ++step) do_step(step);
     }
 
     // ---- the streams' parts of each pair become one, through LDS, and leave as
     // whole rows
+    float factor = 1.0f;  // of this lane's part of its pair
     {
-      const float sum = pair_sum<S::kWide>(l);
+      const float sum = pair_sum<S::kWide>(l), kept = pair_sum<S::kWide>(l_kept);
       if (lane < S::kWavePairs) s_ml[wave][lane] = make_float2(m, sum);
+      if (kept > 0.0f) factor = sum / kept;  // (no key, or NaN, otherwise)
     }
     wait_and_barrier<0>();  // every wave has left the ring, its last loads have ended, and s_ml is complete
     float* piece = nullptr;
@@ -1144,7 +1170,6 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       const int64_t id = KIND == kShared ? static_cast<int64_t>(w) + item : (lo == 0 ? 2 * w + 1 : 2 * w);
       piece = pieces + id * piece_floats(M);
     }
-    float factor = 0.0f;  // of this lane's part of its pair
     {
       const int first = pg * S::kStreams;
       float top = kMInit, sum = 0.0f;
@@ -1155,7 +1180,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         const float2 ml = s_ml[first + k][col];
         sum += ml.y * __builtin_amdgcn_exp2f(ml.x - top);
       }
-      factor = __builtin_amdgcn_exp2f(m - top);
+      factor *= __builtin_amdgcn_exp2f(m - top);
       const int local = pg * S::kWavePairs + col;
       if (whole) {
         factor = sum == 0.0f ? 0.0f : factor / sum;

@@ -70,3 +70,40 @@ def test_values_of_any_size(gpu, heads, width, size, form):
     out, lse = call(gpu, b, form, 1)
     assert torch.isfinite(out).all()
     b.check(out, lse)
+
+
+@FORMS
+@TILES
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_outweighing_key(gpu, dtype, heads, width, form):
+    """One key outweighs the others by a fraction of a power of two more than a
+    whole number, so that its softmax weight is not representable in 16 bits:
+    the weight's rounding has to cancel in the quotient.
+
+    Bound: with weights p_s (1 + d_s), |d_s| <= u = half a step of the type, in
+    numerator and normaliser, the quotient is off by at most the sum of
+    p_s |d_s| |v_s - out| / (1 - u); scores and exponentials are off by dz each;
+    64 float32 roundings of the sums; then the output's own rounding.  The log
+    of the sum does not see the weights' rounding."""
+    announce(f"{form} attention heads={heads} width={width} {dtype} outweighing key")
+    rises = [0.4, 1.3, 2.7, 5.5, 9.3, 12.4, 14.2, 15.7]  # powers of two
+    lens = [140 + 9 * r for r in range(len(rises))]
+    # (a key behind each live one lies in the same 16 keys of a step)
+    live = {5: lambda r: 0.0, 69: lambda r: 0.0, 133: lambda r: rises[r] * np.log(2)}
+    b = scored(211, heads, lens, lambda r, s: live[s](r) if s in live else -300.0, lambda r, s: 1.0, dtype, width, 1)
+    out, lse = call(gpu, b, form, 1)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    e, u = L.HALF_STEP["fp32"], L.HALF_STEP[dtype]
+    flat = b.cache.view(-1, 576)
+    at = np.array(sorted(live))
+    for r in range(len(lens)):
+        keys = flat[torch.from_numpy(b.slots(r, at))].double().numpy()
+        want, wl, _, _ = L.attend_row(b.q[r].double().numpy(), keys, at, SCALE, dtype=dtype)
+        z = SCALE * (b.q[r].double().numpy() @ keys.T)
+        p = np.exp(z - wl[:, None])
+        dz = 8 * e * np.abs(z).max(1) + 8 * e
+        off = (p[:, :, None] * np.abs(keys[None, :, :512] - want[:, None])).sum(1)
+        inner = (1.01 * u + 2 * dz[:, None]) * off + 64 * e * (p @ np.abs(keys[:, :512]))
+        bad = ~(np.abs(out[r] - want) <= inner + u * (np.abs(want) + inner))
+        assert not bad.any(), f"row {r}: {bad.sum()} of {bad.size} outputs off"
+        assert (np.abs(lse[r] - wl) <= 16 * e * (np.abs(z).max(1) + 16)).all()
