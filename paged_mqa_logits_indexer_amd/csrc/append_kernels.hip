@@ -5,9 +5,10 @@
 // by that position's angle: (a, b) -> (a c - b s, b c + a s), the 32 cosines
 // and 32 sines of p read from a table row.  The pairs are (i, i + 32), or
 // (2i, 2i + 1) with `interleaved`.  The products of two 24-bit values are
-// exact in float64, so the rotation is computed there and rounded once: an
-// FP8 or E2M1 code next to a rounding border comes out as the definition
-// says, and float64 costs nothing here (all three kernels only move bytes).
+// exact in float64, so the rotation is computed there, and where the result
+// comes to lie on a rounding border, what was lost on the way decides: a rotated
+// value is rounded once, and a code or a 16-bit value comes out as the definition
+// says.  Float64 costs nothing here (all three kernels only move bytes).
 //
 //   index_k_append        FP8: scale = max|y| / 448 (float32), E4M3 codes of
 //                         y / scale, nearest even; a token with a NaN or an
@@ -66,14 +67,65 @@ __device__ __forceinline__ F32Row load8(const char* p) {
   return r;
 }
 
-// a c - b s (or, with s negated, b c + a s with the roles exchanged), rounded
-// once to float32: both products are exact in float64.
-__device__ __forceinline__ float turn(float a, float c, float b, float s) {
-  return static_cast<float>(static_cast<double>(a) * c - static_cast<double>(b) * s);
+// a c - b s (or, with s negated, b c + a s with the roles exchanged) in float64:
+// two exact products and one rounding.
+__device__ __forceinline__ double turn(float a, float c, float b, float s) {
+  return static_cast<double>(a) * c - static_cast<double>(b) * s;
 }
 
-// Rotates dimensions 8 piece .. 8 piece + 7 of the 64 (x) in place; `partner`
-// holds the same elements of the other half (unused when interleaved).
+// The same rounded to odd: the nearest value, or its neighbour on the other side
+// of the exact one where that is inexact and the nearest one's last bit is clear.
+// A rounding to at most 51 bits of it is that of the exact value.  `lost`, what
+// the sum's rounding took away, is exact.
+__device__ __forceinline__ double turn_odd(float a, float c, float b, float s) {
+  const double p = static_cast<double>(a) * c, q = -static_cast<double>(b) * s;
+  const double sum = p + q, part = sum - p;
+  const double lost = (p - (sum - part)) + (q - part);
+  uint64_t bits = __builtin_bit_cast(uint64_t, sum);
+  if ((lost < 0.0 || lost > 0.0) && !(bits & 1)) bits += (lost > 0.0) == (sum > 0.0) ? 1 : -1;  // (not for NaN)
+  return __builtin_bit_cast(double, bits);
+}
+
+// Whether y (float64, within half a step of its last bit) may round otherwise
+// than the exact value does when it is rounded to TO, by way of float32 f for the
+// 16-bit types: where y, or f, lies half-way between two values of TO.  Below
+// the smallest normal value half-way lies elsewhere; there, always.  (One random
+// value in 2^29, 2^16 and 2^13.)
+template <int TO>
+__device__ __forceinline__ bool on_border(double y, float f) {
+  const uint32_t bits = __float_as_uint(f);
+  if constexpr (TO == IDX_BF16) return (bits & 0xFFFFu) == 0x8000u;  // (its subnormals are float32's)
+  if constexpr (TO == IDX_FP16) return (bits & 0x1FFFu) == 0x1000u || (fabsf(f) < 0x1p-14f && f != 0.0f);
+  return (static_cast<uint32_t>(__builtin_bit_cast(uint64_t, y)) & 0x1FFFFFFFu) == 0x10000000u ||
+         (fabsf(f) < 0x1p-126f && y != 0.0);
+}
+
+// float32 of x: rounded to nearest, or, if it is rounded to 16 bits next, to odd.
+template <int TO>
+__device__ __forceinline__ float narrow(double x) {
+  const float f = static_cast<float>(x);
+  if constexpr (TO == IDX_FP32) return f;
+  uint32_t bits = __float_as_uint(f);
+  const double back = f;
+  if ((back < x || back > x) && !(bits & 1)) bits += fabs(back) < fabs(x) ? 1 : -1;
+  return __uint_as_float(bits);
+}
+
+// a c - b s as a float32 value whose rounding to TO is the rounding of the exact
+// one.  (Without the branch, 8192 latent rows 5.5 -> 8.3 us; with one branch for
+// the eight values of a lane, whose factors all stay in registers for it, 6.2.)
+template <int TO>
+__device__ __forceinline__ float turned(float a, float c, float b, float s) {
+  const double y = turn(a, c, b, s);
+  const float f = static_cast<float>(y);
+  if (__builtin_expect(on_border<TO>(y, f), false)) return narrow<TO>(turn_odd(a, c, b, s));
+  return f;
+}
+
+// Rotates dimensions 8 piece .. 8 piece + 7 of the 64 (x) in place, for rounding
+// to TO; `partner` holds the same elements of the other half (unused when
+// interleaved).
+template <int TO>
 __device__ __forceinline__ void rotate8(F32Row& x, const F32Row& partner, int piece, bool interleaved,
                                         const float* __restrict__ table) {
   if (interleaved) {
@@ -82,8 +134,8 @@ __device__ __forceinline__ void rotate8(F32Row& x, const F32Row& partner, int pi
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float a = x.v[2 * i], b = x.v[2 * i + 1];
-      x.v[2 * i] = turn(a, c[i], b, s[i]);
-      x.v[2 * i + 1] = turn(b, c[i], a, -s[i]);
+      x.v[2 * i] = turned<TO>(a, c[i], b, s[i]);
+      x.v[2 * i + 1] = turned<TO>(b, c[i], a, -s[i]);
     }
   } else {
     const float* ct = table + 8 * (piece & 3);
@@ -93,8 +145,8 @@ __device__ __forceinline__ void rotate8(F32Row& x, const F32Row& partner, int pi
     const f32x4 s1 = reinterpret_cast<const f32x4*>(ct + kHalfRope)[1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x.v[i] = turn(x.v[i], c0[i], partner.v[i], sign * s0[i]);
-      x.v[4 + i] = turn(x.v[4 + i], c1[i], partner.v[4 + i], sign * s1[i]);
+      x.v[i] = turned<TO>(x.v[i], c0[i], partner.v[i], sign * s0[i]);
+      x.v[4 + i] = turned<TO>(x.v[4 + i], c1[i], partner.v[4 + i], sign * s1[i]);
     }
   }
 }
@@ -137,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void index_k_append_kernel(
   F32Row x = load8<DT>(row + piece * 8 * kBytes);
   if (piece < kRope / 8) {
     const F32Row other = load8<DT>(row + (piece ^ 4) * 8 * kBytes);
-    rotate8(x, other, piece, interleaved != 0, rope + static_cast<int64_t>(pos) * kRope);
+    rotate8<IDX_FP32>(x, other, piece, interleaved != 0, rope + static_cast<int64_t>(pos) * kRope);
   }
   uint32_t amax = amax_bits(x);
   amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 1)));
@@ -199,10 +251,10 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(
     return;
   }
   const int pos = max(0, min(positions[token], max_positions - 1));
-  const int turned = piece - kLatentPieces;
+  const int rotated = piece - kLatentPieces;
   F32Row x = load8<DT>(row + piece * 16);
   const F32Row other = load8<DT>(row + (piece ^ 4) * 16);
-  rotate8(x, other, turned, interleaved != 0, rope + static_cast<int64_t>(pos) * kRope);
+  rotate8<DT>(x, other, rotated, interleaved != 0, rope + static_cast<int64_t>(pos) * kRope);
   i32x4 y;
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = static_cast<int>(bits16<DT>(x.v[2 * i]) | (bits16<DT>(x.v[2 * i + 1]) << 16));
