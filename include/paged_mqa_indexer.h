@@ -518,7 +518,8 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * infinities included, does not reach that row.  A row that sees a NaN, whose
  * scale * q . k_s is +infinity, or -infinity under a softcap, is NaN.  Without
  * a softcap a score of -infinity has the weight zero, and outputs at which such
- * a key's value is infinite may be NaN.
+ * a key's value is infinite may be NaN.  (Scores are held in powers of two and
+ * finite up to a magnitude of 2^127; finite ones take part however low they are.)
  *
  * q            (device) [rows][heads][576], dtype BF16 or FP16, 16-B aligned
  * latent_pages (device) [num_pages][64][576] of the same type, 16-B aligned

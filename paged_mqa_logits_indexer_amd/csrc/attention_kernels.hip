@@ -51,7 +51,7 @@ constexpr int kRingBytes = 2 * kTile * kRowBytes;  // 147456: 128 keys in all sl
 constexpr int kWindow = 2048;                      // sparse: keys whose cache rows are resolved at a time
 constexpr int kAttnThreads = 256;
 constexpr int kScanChunks = 1056;                  // work-list chunks of 256 pair tiles
-constexpr float kMInit = -1.7e38f;                 // running maximum before any key (finite: no inf - inf)
+constexpr float kMInit = -__FLT_MAX__;             // running maximum before any key: no finite score is below it (finite: no inf - inf)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 typedef short s16x4 __attribute__((ext_vector_type(4)));

@@ -107,3 +107,24 @@ def test_outweighing_key(gpu, dtype, heads, width, form):
         bad = ~(np.abs(out[r] - want) <= inner + u * (np.abs(want) + inner))
         assert not bad.any(), f"row {r}: {bad.sum()} of {bad.size} outputs off"
         assert (np.abs(lse[r] - wl) <= 16 * e * (np.abs(z).max(1) + 16)).all()
+
+
+@FORMS
+@TILES
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_scores_next_to_the_lowest(gpu, dtype, heads, width, form):
+    """Rows whose scores are all finite but lie in the last octave above the
+    lowest float32: the nearest key under the steepest bias outweighs the rest."""
+    announce(f"{form} attention heads={heads} width={width} {dtype} lowest scores")
+    lens = [70, 1, 140, 65]
+    b = scored(221, heads, lens, lambda r, s: 0.0, lambda r, s: 1.0, dtype, width, 1 if form == "shared" else 0)
+    far = 1 << 20
+    slopes = np.linspace(1.14e32, 2.2e32, heads).astype(np.float32)  # times the distance, in powers of two: 1.7e38 .. 3.3e38
+    out, lse = call(gpu, b, form, 1, slopes=b.dev(slopes), row_positions=b.dev(np.full(len(lens), far, np.int32)))
+    flat = b.cache.view(-1, 576)
+    for r, n in enumerate(lens):
+        key = flat[torch.from_numpy(b.slots(r, np.array([n - 1])))][0, :512]
+        assert torch.equal(out[r].cpu(), key.expand(heads, 512)), f"row {r}"
+        # float32 roundings of slope, distance, score, maximum and the way back
+        want = -slopes.astype(np.float64) * (far - n + 1)
+        assert (np.abs(lse[r].double().cpu().numpy() - want) <= 8 * L.HALF_STEP["fp32"] * np.abs(want)).all(), f"row {r}"
