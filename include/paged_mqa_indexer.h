@@ -532,8 +532,10 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  *              belongs to request r / next_n.  next_n 0 and cu_q (device)
  *              int32 [requests + 1], ascending: request b owns rows cu_q[b] ..
  *              cu_q[b+1]-1; rows of no request are not written.
- * scale        finite; softcap finite, >= 0, and scale / softcap finite
- * slopes       (device) float [heads], or NULL: no distance bias
+ * scale        magnitude at most 2^127; softcap 0 .. 2^127, and scale / softcap
+ *              finite
+ * slopes       (device) float [heads] of magnitudes up to 2^127, or NULL: no
+ *              distance bias
  * row_positions(device) int32 [rows] within +-2^30, or NULL: row_lens - 1
  * out          (device) [rows][heads][512] of q's type, 16-B aligned
  * lse          (device) float [rows][heads], or NULL

@@ -404,7 +404,8 @@ static idx_status check_attention(const pmqa::AttentionArgs& a, const void* keys
     return IDX_EINVAL;
   if ((a.cu_q != nullptr) == (a.next_n > 0)) return IDX_EINVAL;
   if (!a.cu_q && static_cast<int64_t>(a.requests) * a.next_n != a.rows) return IDX_EINVAL;
-  if (!std::isfinite(a.scale) || !std::isfinite(a.softcap) || a.softcap < 0.0f) return IDX_EINVAL;
+  // (both are multiplied by log2(e) in float32; comparisons that NaN fails)
+  if (!(std::fabs(a.scale) <= 0x1p127f) || !(a.softcap >= 0.0f && a.softcap <= 0x1p127f)) return IDX_EINVAL;
   if (a.softcap > 0.0f && !std::isfinite(a.scale / a.softcap)) return IDX_EINVAL;
   if (a.dtype != IDX_BF16 && a.dtype != IDX_FP16) return IDX_EUNSUPPORTED;
   if (a.rows > IDX_MAX_ROWS || a.heads > IDX_MAX_ATTENTION_HEADS || a.requests > IDX_MAX_REQUESTS ||
