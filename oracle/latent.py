@@ -137,3 +137,54 @@ def attend_row(q, keys, at, scale, softcap=0.0, slopes=None, position=0, dtype="
     rel = u + 4 * dz + (2 * n + 16) * e
     bound = u * np.abs(out) + rel[:, None] * spread + tiny + u * rel[:, None] * spread
     return out, lse, bound, dz + (n + 8) * e + 4 * e * np.abs(lse)
+
+
+def attend_row_rms(q, keys, at, scale, softcap=0.0, slopes=None, position=0, dtype="bf16"):
+    """attend_row's values with what their errors should amount to, instead of
+    what they can at worst: (out, lse, rms allowance [heads], lse allowance
+    [heads]).  The first allowance is of the root mean square over the 512
+    dimensions of a head's error; u and e as in attend_row:
+
+      output    rounded by up to u |out| in each dimension, evenly in between:
+                u |out| / sqrt(3) over the dimensions
+      weights   rounded by d_s, |d_s| <= u, in sum and divisor: the error vector
+                is sum p_s d_s (v_s - out), and where the values of different
+                keys are as good as orthogonal its square is at most
+                u^2 sum p_s^2 |v_s - out|^2  (these two: root of the sum of squares)
+      scores    a float32 sum of 576 terms t_i walks at random: its steps are
+                rounded by e times partial sums of about sqrt(i) |t| / sqrt(576),
+                together 24 e |t| / sqrt(2); twice that, 8 e |z| for the factors
+                and the exponential, 16 e softcap for tanh =: dz_s, moving the
+                output by sum p_s dz_s |v_s - out|
+      sums      of n terms that walk at random too: (4 sqrt(n) + 16) e of
+                |out| + sqrt(sum p_s^2 |v_s|^2); FP16's smallest weights are
+                rounded by 2^-33 of the largest
+      all       10 % more, for values that are not quite orthogonal
+    """
+    q, keys = np.asarray(q, np.float64), np.asarray(keys, np.float64)
+    out, lse, _, _ = attend_row(q, keys, at, scale, softcap, slopes, position, dtype)
+    heads, n = q.shape[0], keys.shape[0]
+    if n == 0:
+        return out, lse, np.zeros(heads), np.zeros(heads)
+    e, u = HALF_STEP["fp32"], HALF_STEP[dtype]
+    z = scale * (q @ keys.T)
+    dz = 2 * 24 / 2 ** 0.5 * e * abs(scale) * np.sqrt(q ** 2 @ (keys ** 2).T)
+    if softcap:
+        z = softcap * np.tanh(z / softcap)
+        dz = dz + 16 * e * softcap
+    if slopes is not None:
+        far = np.asarray(slopes, np.float64)[:, None] * np.abs(position - np.asarray(at, np.float64))[None, :]
+        z = z - far
+        dz = dz + 4 * e * far
+    dz = dz + 8 * e * np.abs(z)
+    p = np.exp(z - lse[:, None])
+    v = keys[:, :LATENT_DIM]
+    # |v_s - out_h|^2 of every key and head
+    apart = np.maximum((v ** 2).sum(1)[None, :] - 2 * out @ v.T + (out ** 2).sum(1)[:, None], 0.0)
+    size = np.sqrt((v ** 2).sum(1))
+    walk = np.sqrt((out ** 2).sum(1)) + np.sqrt(p ** 2 @ size ** 2)
+    tiny = n ** 0.5 * 2.0 ** -33 * p.max(1) * size.max() if dtype == "fp16" else 0.0
+    rounding = u * np.sqrt((out ** 2).sum(1) / 3 + (p ** 2 * apart).sum(1))
+    rest = (p * dz * np.sqrt(apart)).sum(1) + (4 * n ** 0.5 + 16) * e * walk + tiny
+    allowed = 1.1 * (rounding + rest) / LATENT_DIM ** 0.5
+    return out, lse, allowed, (p * dz).sum(1) + (4 * n ** 0.5 + 16) * e + 4 * e * np.abs(lse)
