@@ -464,8 +464,9 @@ idx_status topk_rows_f16(const uint16_t* logits, int64_t logits_stride,
  * index_k_append -- index keys as FP8 E4M3FN codes with one scale per token,
  * the layout indexer_logits reads: y = the key with dimensions 0..63 rotated,
  * scale = max|y| / 448 (float32; 0 for a key of zeros), code = e4m3(y / scale)
- * to nearest even.  A key with a NaN or an infinity gets codes 0 and the
- * scale NaN: its logits are NaN, which topk_rows never selects.
+ * to nearest even, of the float32 quotient.  A key with a NaN or an infinity
+ * gets codes 0 and the scale NaN: its logits are NaN, which topk_rows never
+ * selects.
  *
  * k            (device) [tokens] rows of 128, k_dtype BF16, FP16 or FP32
  * kv_pages     (device) uint8 [num_pages][64][128], 16-B aligned
@@ -480,7 +481,9 @@ idx_status index_k_append(const void* k, int64_t k_stride, int32_t k_dtype, cons
  * indexer_logits_mxfp4 reads: per block of 32 dimensions the power of two
  * 2^(floor(log2 max|y|) - 2) as an E8M0 byte (at least 2^-127) and E2M1 codes
  * of y over it, to nearest even, magnitudes above 6 to 6.  A block with a NaN
- * or an infinity gets codes 0 and the byte 255 (NaN).
+ * or an infinity gets codes 0 and the byte 255 (NaN).  Unlike an FP8 key, such a
+ * key can be selected: the NaN stands inside the logits' ReLU, whose max(0, NaN)
+ * is 0, so its logits are 0.  A caller that may meet such keys keeps them out.
  *
  * kv_pages     (device) uint8 [num_pages][64][68], 16-B aligned
  */
@@ -512,9 +515,10 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * lse = -infinity.  Key s of a request is slot s % 64 of page
  * block_table[request][s / 64].  Products and the softmax are summed in
  * float32; the softmax weights are rounded to the cache's type for the product
- * with the values.  The sum is divided at its end: a row is finite as long as
- * the magnitudes of its finite keys' values add up to less than 2^127 (always,
- * in FP16).  What the cache holds at keys a row does not see, NaN and
+ * with the values, which is divided by the sum of the rounded weights (lse takes
+ * them unrounded).  It is divided at the end: a row is finite as long as the
+ * magnitudes of its finite keys' values add up to less than 2^127 (always, in
+ * FP16).  What the cache holds at keys a row does not see, NaN and
  * infinities included, does not reach that row.  A row that sees a NaN, whose
  * scale * q . k_s is +infinity, or -infinity under a softcap, is NaN.  Without
  * a softcap a score of -infinity has the weight zero, and outputs at which such
@@ -527,7 +531,11 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * requests     1 .. IDX_MAX_REQUESTS; rows 1 .. IDX_MAX_ROWS;
  *              heads 1 .. IDX_MAX_ATTENTION_HEADS;
  *              num_pages 1 .. IDX_MAX_CACHE_PAGES; max_pages 1 ..
- *              IDX_MAX_ATTENTION_PAGES, requests * max_pages < 2^31
+ *              IDX_MAX_ATTENTION_PAGES, requests * max_pages < 2^31.  Over
+ *              whole pages and shared prefixes the host sizes the work by
+ *              max_pages, as it does not know the lengths: short requests in a
+ *              wide table take longer than in a narrow one (same results within
+ *              rounding)
  * next_n, cu_q next_n > 0 and cu_q NULL: rows = requests * next_n, row r
  *              belongs to request r / next_n.  next_n 0 and cu_q (device)
  *              int32 [requests + 1], ascending: request b owns rows cu_q[b] ..
@@ -540,8 +548,8 @@ idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const
  * out          (device) [rows][heads][512] of q's type, 16-B aligned
  * lse          (device) float [rows][heads], or NULL
  * workspace    (device) scratch of at least attention_workspace_bytes(rows,
- *              heads, requests) bytes, 256-B aligned; needs no initialisation.
- *              Calls that share a workspace must be ordered on one stream.
+ *              heads, requests) bytes (at most 135 MB), 256-B aligned; needs no
+ *              initialisation.  Calls that share a workspace must be ordered on one stream.
  * Errors: IDX_EINVAL (NULL pointer, non-positive size, next_n and cu_q both or
  * neither, rows != requests * next_n, scale or softcap), IDX_EUNSUPPORTED
  * (type, limits), IDX_EALIGN, IDX_EWORKSPACE, IDX_ELAUNCH.
@@ -567,7 +575,10 @@ idx_status paged_attention(const void* q, const void* latent_pages, int32_t dtyp
  * block-table row are the same (those of row 0 are used).  The shared keys are
  * read once for the rows of all requests.  Arguments and results as for
  * paged_attention with next_n rows per request; the workspace holds
- * shared_prefix_workspace_bytes(rows, heads, requests).
+ * shared_prefix_workspace_bytes(rows, heads, requests), which grows with the
+ * batch: 2.1 KB for each row and head, as much again with every request's
+ * next_n * heads rounded up to 128, and 68 MB (a million rows and heads of
+ * requests with 128 each: 4.4 GB; 4096 requests of one row and head: 1.2 GB).
  *
  * prefix_pages 1 .. max_pages
  */

@@ -665,7 +665,9 @@ def index_k_append(k, positions, slots, rope, kv_pages, k_scales, interleaved=Fa
 
 
 def index_k_append_mxfp4(k, positions, slots, rope, kv_pages, interleaved=False, events=None):
-    """index_k_append into packed MXFP4 tokens: kv_pages [P, 64, 68] uint8."""
+    """index_k_append into packed MXFP4 tokens: kv_pages [P, 64, 68] uint8.  A key
+    with a NaN or an infinity has logits of 0 here, which can be selected (an FP8
+    key's are NaN, which cannot): keep such keys out."""
     _need_shaped(kv_pages, "kv_pages", torch.uint8, k.device, (kv_pages.shape[0], PAGE_TOKENS, MXFP4_TOKEN_BYTES))
     _append_call("index_k_append_mxfp4", HEAD_DIM, (torch.bfloat16, torch.float16, torch.float32), k, positions,
                  slots, rope, kv_pages, (), interleaved, events)
@@ -755,7 +757,9 @@ def paged_attention(q, latent_pages, block_table, row_lens, next_n, scale, out, 
     row_starts[r] (default 0) up to row_lens[r].  next_n rows per request, or
     next_n = 0 with cu_q [requests + 1] int32 for a ragged batch.  Scores are
     scale q . k, then softcap * tanh(z / softcap) if softcap > 0, then minus
-    slopes[h] * |row_positions[r] - s| (default position row_lens - 1).
+    slopes[h] * |row_positions[r] - s| (default position row_lens - 1).  The work
+    is sized by the block table's width, so a table much wider than the rows'
+    lengths costs time.
     out [rows, heads, 512] of q's type; lse [rows, heads] float32 or None.  A
     row that sees no key gets out 0 and lse -inf.
 
@@ -772,7 +776,9 @@ def shared_prefix_attention(q, latent_pages, block_table, row_lens, next_n, pref
                             events=None):
     """paged_attention for a batch whose requests' first ``prefix_pages`` pages
     are the same (the first entries of every block_table row): their keys are
-    read once for all rows.  Workspace: shared_prefix_workspace_bytes()."""
+    read once for all rows.  Workspace: shared_prefix_workspace_bytes(), which
+    grows with the batch (about 4 KB for each row and head, with every request's
+    rows times heads rounded up to 128) and is allocated for the call when None."""
     _attention_call("shared_prefix_attention", q, latent_pages, block_table, row_lens, next_n, None, row_starts,
                     prefix_pages, scale, out, lse, softcap, slopes, row_positions, workspace, events)
 

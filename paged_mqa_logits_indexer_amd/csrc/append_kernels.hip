@@ -22,8 +22,9 @@
 //
 // Every lane moves 16-byte pieces and no lane waits for another token's, so
 // the kernels are bound by memory (and, for a few tokens, by one dependent
-// load chain: slot and position, then the table row).  Measured: 8192 latent
-// rows 6.1 us (21 MB, 3.4 TB/s), 8191 MXFP4 keys 3.9 us, 8 FP8 keys 2.1 us.
+// load chain: slot and position, then the table row).  Measured (medians of 25
+// under the kernel trace): 8192 latent rows 6.8 us (21 MB, 3.1 TB/s), 8191 MXFP4
+// keys 4.8 us, 8 FP8 keys 2.5 us.
 #include "indexer_common.h"
 #include "launches.h"
 

@@ -23,12 +23,13 @@
 // workspace as (o, m, l) in float32 and a second kernel joins them, in a fixed
 // order.
 //
-// Measured (MI355X, kernel alone): 64 requests of 1 .. 32768 keys with 16 heads
-// 47 us (a K stream of 240 MB in about 35 us, the rest each workgroup's start
-// and end); 1024 rows of 128 heads over 2048 selected keys 611 us (625 TFLOP/s;
-// the library's 8192^3 product reaches 1193), the MFMAs busy 43 % of all cycles
-// and 55 - 60 % within a step; 8 requests on 32768 shared keys 92 us; one
-// request of 65 keys 9.3 us, five dependent round trips to memory.
+// Measured (MI355X, medians of 25 under the kernel trace): 64 requests of 1 ..
+// 32768 keys with 16 heads 54 us (a K stream of 240 MB in about 35 us, the rest
+// each workgroup's start and end); 1024 rows of 128 heads over 2048 listed keys
+// 634 us (584 GFLOP, 920 TFLOP/s; the library's 8192^3 product reaches 1193), the
+// MFMAs busy 42 % of all cycles -- a third of that case's 64-key tiles hold nothing
+// but padding, which is multiplied like keys; 8 requests on 32768 shared keys
+// 97 us; one request of 65 keys 9.3 us, five dependent round trips to memory.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -565,7 +566,8 @@ __host__ __device__ __forceinline__ int64_t piece_floats(int m) { return static_
 // arithmetic, and 32 keys per step in 4 slots: the value product of a step runs
 // after the next step's scores, between whose MFMAs its weights are computed,
 // and two steps of loads are ahead.  (1024 rows of 128 heads over 2048 selected
-// keys, calls in a row: 624 us, with 64-pair tiles of the narrow form 793.)
+// keys, calls in a row on the same card: 624 us, with 64-pair tiles of the narrow
+// form 793.)
 template <int M>
 struct Shape {
   static constexpr bool kWide = M == 128;
@@ -1399,7 +1401,9 @@ int64_t pairs_together(const AttentionArgs& a) {
 // 367 / 296 / 203; 64 heads, 256 rows 354 / 188 / 152 / 180; 16 requests of
 // 8192 keys with 128 heads 112 / 85 / 103 / 121, of 32768 keys 396 / 265 / 268
 // / 221.  (For whole pages the table's width stands for the lengths, which the
-// host does not know.)  Tiles wider than the pairs would only idle.
+// host does not know; the times are of tables as wide as the requests, and in a
+// wider one the choice falls on larger tiles than those would take.)  Tiles wider
+// than the pairs would only idle.
 template <int KIND>
 int tile_pairs(const AttentionArgs& a) {
   constexpr int kSizes[] = {16, 32, 64, 128};
