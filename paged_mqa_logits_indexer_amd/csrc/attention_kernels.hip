@@ -247,6 +247,15 @@ __device__ __forceinline__ float pair_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// Softmax weight of score z (powers of two) under the maximum m.  The maximum is
+// that of the rounded scores, so the subtraction is not contracted with the
+// multiplication that made z: from 2^31 on, what that rounds away is itself
+// hundreds of powers of two.
+__device__ __forceinline__ float weight(float z, float m) {
+#pragma clang fp contract(off)
+  return __builtin_amdgcn_exp2f(z - m);
+}
+
 // tanh(x) = 1 - 2 / (1 + e^2x): absolute error of about one float32 step of 1,
 // which the cap's factor turns into that of the score; near zero, where the
 // difference would lose the argument's digits, the odd series
@@ -633,8 +642,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   const int capacity = a.max_pages * kPage;
   const char* cache = static_cast<const char*>(a.cache);
   const float to_log2 = a.scale * kLog2e;
-  // wide: the factor is applied with the exponential's subtraction, unless the
-  // score is changed in between (or the factor turns the order round)
+  // wide: the factor is applied where the maximum is taken, unless the score is
+  // changed before (or the factor turns the order round)
   const bool prescale = a.softcap > 0.0f || a.slopes || !(to_log2 > 0.0f);
   const float z_scale = prescale ? 1.0f : to_log2;
 
@@ -826,8 +835,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
 #pragma unroll
     for (int i = 0; i < kScores; ++i) z_before[i] = -__builtin_inff();
     auto weigh = [&](int i, float& sum) {  // scores 2 i and 2 i + 1
-      const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(z_before[2 * i], z_scale, -m));
-      const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(z_before[2 * i + 1], z_scale, -m));
+      const float e0 = weight(z_before[2 * i], m), e1 = weight(z_before[2 * i + 1], m);
       sum += e0 + e1;
       int both = E::round2(e0, e1);
       __asm__ volatile("" : "+v"(both), "+v"(sum));  // computed here, between the MFMAs, and not where it is used
@@ -1048,12 +1056,15 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         // pair tile sees or whose non-finite values have been cleared.)
         float mx = -__builtin_inff(), kept = 0.0f;
         value_wide(step > step0 ? ring + ((step - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes : base, [&](int d) {
-          if (d < 8)
+          if (d < 8) {
+            z[2 * d] *= z_scale;
+            z[2 * d + 1] *= z_scale;
             mx = fmaxf(mx, fmaxf(z[2 * d], z[2 * d + 1]));
-          else
+          } else {
             keep(d - 8, kept);
+          }
         });
-        mx = pair_max<true>(mx) * z_scale - E::kShift;
+        mx = pair_max<true>(mx) - E::kShift;
         const float raised = mx > m + E::kRaise ? mx : m;
         const bool any_raised = step > step0 && __ballot(raised != m) != 0;  // nothing to rescale in the first step
         by = __builtin_amdgcn_exp2f(m - raised);
@@ -1084,7 +1095,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         for (int st = 0; st < ST; ++st) {
           float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f(z[st * 4 + i] - m);
+          for (int i = 0; i < 4; ++i) e[i] = weight(z[st * 4 + i], m);
           l += (e[0] + e[1]) + (e[2] + e[3]);
           const int2 both = make_int2(E::round2(e[0], e[1]), E::round2(e[2], e[3]));
           l_kept += E::add2(both.x, E::add2(both.y, 0.0f));

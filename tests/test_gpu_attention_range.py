@@ -128,3 +128,28 @@ def test_scores_next_to_the_lowest(gpu, dtype, heads, width, form):
         # float32 roundings of slope, distance, score, maximum and the way back
         want = -slopes.astype(np.float64) * (far - n + 1)
         assert (np.abs(lse[r].double().cpu().numpy() - want) <= 8 * L.HALF_STEP["fp32"] * np.abs(want)).all(), f"row {r}"
+
+
+@FORMS
+@TILES
+@pytest.mark.parametrize("power", [20, 33, 66, 123])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(gpu, heads, width, sign, power, form):
+    """Scores so large that float32's steps there are many powers of two: the
+    keys of a row's largest score share all its weight, wherever they stand."""
+    announce(f"{form} attention heads={heads} width={width} scores of {sign} * 2^{power}")
+    lens = [333, 1, 70, 140, 200]
+    score = lambda r, s: sign * 2.0 ** power * (1 + (37 * s % 128) / 128)  # a BF16 value, every 128 keys again
+    b = scored(231, heads, lens, score, lambda r, s: 1.0, width=width, shared=1 if form == "shared" else 0)
+    out, lse = call(gpu, b, form, 1)
+    e, u = L.HALF_STEP["fp32"], L.HALF_STEP["bf16"]
+    flat = b.cache.view(-1, 576)
+    for r, n in enumerate(lens):
+        at = np.arange(n)
+        z = np.array([score(r, s) for s in at])
+        top = flat[torch.from_numpy(b.slots(r, at[z == z.max()]))][:, :512].double().numpy()
+        want = np.broadcast_to(top.mean(0), (heads, 512))
+        bad = ~(np.abs(out[r].double().cpu().numpy() - want) <= u * np.abs(want) + 16 * e * np.abs(top).max(0))
+        assert not bad.any(), f"row {r}: {bad.sum()} of {bad.size} outputs off"
+        zh = SCALE * b.q[r, :, 512].double().numpy() * z.max()
+        assert (np.abs(lse[r].double().cpu().numpy() - zh) <= 8 * e * np.abs(zh) + 2).all(), f"row {r}"
