@@ -83,6 +83,13 @@ typedef enum { IDX_BF16 = 0, IDX_FP16 = 1, IDX_FP32 = 2 } idx_value_dtype;
 #define IDX_LATENT_DIM 512
 #define IDX_ROPE_DIM 64
 #define IDX_LATENT_ROW 576
+/* A latent cache row in 4 bits: 256 bytes of E2M1 codes (dimension 2i in the low
+ * nibble of byte i, 2i + 1 in the high one), 16 E8M0 bytes (byte j: the power of
+ * two of dimensions 32j .. 32j + 31), 64 rotated dimensions in 16 bits each. */
+#define IDX_LATENT_MXFP4_ROW 400
+#define IDX_MAX_AXES 4        /* of positions */
+#define IDX_MAX_CACHES 1024   /* of one copy_pages call */
+#define IDX_MAX_TOKEN_BYTES 16384
 #define IDX_MAX_ATTENTION_HEADS 128
 #define IDX_MAX_APPEND_TOKENS (1 << 24)
 #define IDX_MAX_CACHE_PAGES ((1 << 25) - 1) /* 64 * pages stays a 32-bit integer */
@@ -502,6 +509,160 @@ idx_status index_k_append_mxfp4(const void* k, int64_t k_stride, int32_t k_dtype
 idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const int32_t* positions,
                          const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
                          int32_t tokens, int32_t num_pages, void* latent_pages, void* stream);
+
+/*
+ * latent_append_mxfp4 -- latent_append into 4-bit rows (IDX_LATENT_MXFP4_ROW): the
+ * latent part as E2M1 codes under a power of two per 32 dimensions, chosen and
+ * rounded as index_k_append_mxfp4 does, the rotated part in 16 bits as
+ * latent_append rounds it.  A block with a NaN or an infinity gets codes 0 and the
+ * byte 255: its 32 values are NaN, and so is every row that attends to the key.
+ *
+ * kv           (device) [tokens] rows of 576, dtype BF16 or FP16
+ * latent_pages (device) uint8 [num_pages][64][400], 16-B aligned
+ */
+idx_status latent_append_mxfp4(const void* kv, int64_t kv_stride, int32_t dtype, const int32_t* positions,
+                               const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                               int32_t tokens, int32_t num_pages, uint8_t* latent_pages, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height and width of image and video
+ * tokens): each of the 32 angles belongs to an axis, and a token is turned by
+ * angle i of its position on that axis.  axis_map holds two bits per angle (bits
+ * 2i, 2i + 1: the axis of angle i); text has one axis and the map 0.
+ *
+ * positions    (device) int32 [axes][tokens], clamped to [0, max_positions)
+ * axes         1 .. IDX_MAX_AXES; every angle's axis is below it (else IDX_EINVAL)
+ * rope         (device) float [max_positions][64] as for the appends, 16-B aligned
+ * tokens       1 .. IDX_MAX_APPEND_TOKENS
+ * Errors: IDX_EINVAL (NULL pointer, non-positive size, axes, map, strides),
+ * IDX_EUNSUPPORTED (type, limits), IDX_EALIGN, IDX_ELAUNCH.
+ *
+ * axis_rotations -- every token's cosines and sines in one row:
+ * out[t][i] = rope[positions[axis of i][t]][i], out[t][32 + i] likewise.  The
+ * appends take the result as their table, with max_positions = tokens and
+ * positions 0 .. tokens - 1: one call a step serves the appends of all layers.
+ *
+ * out          (device) float [tokens][64], 16-B aligned, not the table itself
+ */
+idx_status axis_rotations(const int32_t* positions, int32_t axes, uint64_t axis_map, int32_t tokens, const float* rope,
+                          int32_t max_positions, float* out, void* stream);
+
+/*
+ * rotate_queries -- the 64 rotated dimensions of every head of every row, as the
+ * attention's queries need them: out[t][h] = x[t][h] turned by token t's angles,
+ * pairs as for the appends, rounded once to nearest even.  x and out are strided
+ * places of rows of 64, such as a slice of the query projection's output and
+ * dimensions 512 .. 575 of the attention's queries; out may be x (the same pointer
+ * and strides), otherwise they share no element.
+ *
+ * x, out       (device) [tokens][heads] rows of 64, dtype BF16 or FP16, strides in
+ *              elements, not negative; pointers and strides 16-B aligned; the rows
+ *              of out lie apart (else IDX_EINVAL)
+ * heads        1 .. IDX_MAX_ATTENTION_HEADS
+ */
+idx_status rotate_queries(const void* x, int64_t x_token_stride, int64_t x_head_stride, int32_t dtype,
+                          const int32_t* positions, int32_t axes, uint64_t axis_map, const float* rope,
+                          int32_t max_positions, int32_t interleaved, int32_t tokens, int32_t heads, void* out,
+                          int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/*
+ * rotate_index_queries -- the indexer's queries as indexer_logits reads them: the
+ * first 64 of 128 dimensions rotated (rounded once to float32), all of them clamped
+ * to +-448 and rounded to E4M3 codes, nearest even; NaN stays NaN.
+ *
+ * q            (device) [tokens][32] rows of 128, dtype BF16, FP16 or FP32, strides
+ *              as above
+ * codes        (device) uint8 [tokens][32][128], 16-B aligned, not q
+ */
+idx_status rotate_index_queries(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t dtype,
+                                const int32_t* positions, int32_t axes, uint64_t axis_map, const float* rope,
+                                int32_t max_positions, int32_t interleaved, int32_t tokens, uint8_t* codes,
+                                void* stream);
+
+/*
+ * Care of the pages.  One pool of page ids serves the caches of all layers; request
+ * b holds the first ceil(lens[b] / 64) pages of its block-table row, and refs[p]
+ * counts the holders of page p (requests, and whoever else keeps a page): a page
+ * with refs 0 is free.  A caller that gives a request a page for new tokens sets
+ * its refs to 1.  Nothing is read back: the calls find the free pages and the
+ * copies on the GPU, in a fixed order, and hand the copies to copy_pages.
+ * new_lens may be lens and new_refs may be refs; other arguments share no memory.
+ *
+ * block_table  (device) int32 [requests][max_pages]; ids outside the pool are not
+ *              counted and not moved
+ * lens         (device) int32 [requests], clamped to [0, 64 max_pages]
+ * refs         (device) int32 [num_pages]
+ * requests     1 .. IDX_MAX_REQUESTS; num_pages 1 .. IDX_MAX_CACHE_PAGES;
+ *              max_pages 1 .. IDX_MAX_ATTENTION_PAGES, requests * max_pages < 2^31
+ * workspace    (device) scratch of pages_workspace_bytes(requests, num_pages)
+ *              bytes, 256-B aligned; needs no initialisation.  Calls that share a
+ *              workspace must be ordered on one stream.
+ * Errors: IDX_EINVAL (NULL pointer, non-positive size), IDX_EUNSUPPORTED (limits),
+ * IDX_EALIGN, IDX_EWORKSPACE, IDX_ELAUNCH.
+ *
+ * release_pages -- requests with ended[b] != 0 give up their pages: one holder less
+ * for each, new_lens[b] = 0.  The others keep their length.
+ *
+ * ended        (device) int32 [requests]
+ */
+size_t pages_workspace_bytes(int32_t requests, int32_t num_pages);
+
+idx_status release_pages(const int32_t* block_table, const int32_t* lens, const int32_t* ended, int32_t requests,
+                         int32_t max_pages, const int32_t* refs, int32_t num_pages, int32_t* new_lens,
+                         int32_t* new_refs, void* stream);
+
+/*
+ * fork_pages -- request b with parents[b] = p becomes a copy of request p: it shares
+ * p's full pages (one holder more for each), and where p has begun a page, b gets
+ * the lowest free page for it, in which the tokens of p's have to be copied:
+ * src[b], dst[b], tokens[b] name the pages and how many of their first tokens (-1,
+ * -1, 0 for a request that needs no copy), as copy_pages takes them.  Requests are
+ * served in ascending order; one for which no page is left is not forked.  Nor is
+ * one that holds tokens (lens[b] > 0), or whose parent is not in [0, requests).
+ * Lengths are those before the call: a parent that is itself forked has none, and
+ * its child is left empty.  counts: pages taken, and requests that went without.
+ *
+ * block_table  rows of forked requests are written, up to their last page
+ * parents      (device) int32 [requests], negative: none
+ * src, dst, tokens (device) int32 [requests];  counts (device) int32 [2]
+ */
+idx_status fork_pages(int32_t* block_table, const int32_t* lens, const int32_t* parents, int32_t requests,
+                      int32_t max_pages, const int32_t* refs, int32_t num_pages, int32_t* new_lens, int32_t* new_refs,
+                      int32_t* src, int32_t* dst, int32_t* tokens, int32_t* counts, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * compact_pages -- makes the pool dense: with L pages held, the i-th held page from
+ * L on goes to the i-th free page below L (both ascending).  The moves are in src
+ * and dst (-1 behind the last), new_table and new_refs say where everything then
+ * is; copy_pages moves the pages themselves.  counts: L, and the number of moves.
+ * Holders other than the block table find their pages through src and dst.
+ *
+ * new_table    (device) int32 [requests][max_pages], may be block_table
+ * src, dst     (device) int32 [num_pages];  counts (device) int32 [2]
+ */
+idx_status compact_pages(const int32_t* block_table, const int32_t* lens, int32_t requests, int32_t max_pages,
+                         const int32_t* refs, int32_t num_pages, int32_t* new_table, int32_t* new_refs, int32_t* src,
+                         int32_t* dst, int32_t* counts, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * copy_pages -- page src[i] to page dst[i] in every cache, for i < n: the first
+ * tokens[i] tokens of it (clamped to 0 .. 64), or all.  Entries whose src or dst is
+ * not in the pool copy nothing (the -1 padding).  No destination is given twice or
+ * is also a source (as the calls above make them); what such pages then hold is
+ * unspecified.
+ *
+ * caches       (host) n_caches device pointers, 16-B aligned: [num_pages][64] tokens
+ * token_bytes  (host) n_caches sizes of a token, multiples of 4, up to
+ *              IDX_MAX_TOKEN_BYTES (both arrays are read during the call)
+ * n_caches     1 .. IDX_MAX_CACHES
+ * src, dst     (device) int32 [n], n in 1 .. IDX_MAX_CACHE_PAGES
+ * tokens       (device) int32 [n], or NULL: whole pages
+ * count        (device) int32, or NULL: only the first min(n, *count) entries
+ */
+idx_status copy_pages(void* const* caches, const int32_t* token_bytes, int32_t n_caches, int32_t num_pages,
+                      const int32_t* src, const int32_t* dst, const int32_t* tokens, const int32_t* count, int32_t n,
+                      void* stream);
 
 /*
  * Attention over the latent cache.  All heads of a row read the same cache

@@ -14,3 +14,4 @@ from .indexer_oracle import (  # noqa: F401
 from . import candidates  # noqa: F401,E402
 from . import latent  # noqa: F401,E402
 from . import prefill  # noqa: F401,E402
+from . import pages  # noqa: F401,E402

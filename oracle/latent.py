@@ -74,9 +74,10 @@ def fp8_key(y):
 
 
 def mxfp4_key(y):
-    """Packed [..., 68] uint8 token of a rotated float32 key."""
+    """Packed uint8 token of a rotated float32 key (or of a latent part): E2M1 codes,
+    two to a byte, then the E8M0 bytes of its blocks of 32 ([..., 68] of 128)."""
     y = np.asarray(y, np.float32)
-    blocks = y.reshape(y.shape[:-1] + (4, 32)).astype(np.float64)
+    blocks = y.reshape(y.shape[:-1] + (y.shape[-1] // 32, 32)).astype(np.float64)
     bad = ~np.isfinite(blocks).all(-1)
     blocks = np.where(bad[..., None], 0.0, blocks)
     amax = np.abs(blocks).max(-1)
@@ -88,6 +89,37 @@ def mxfp4_key(y):
     codes = np.where(bad[..., None], np.uint8(0), codes).reshape(y.shape)
     scale = np.where(bad, 255, power + 127).astype(np.uint8)
     return np.concatenate([codes[..., 0::2] | (codes[..., 1::2] << 4), scale], -1)
+
+
+def latent_mxfp4_values(rows, dtype):
+    """float64 [n, 576] of 4-bit latent rows uint8 [n, 400]; ``dtype`` ("bf16" or
+    "fp16") is that of the rotated part.  The byte 255 makes its block NaN."""
+    rows = np.asarray(rows, np.uint8)
+    table = np.asarray(e2m1_decode_table(), np.float64)
+    codes = np.stack([rows[:, :256] & 15, rows[:, :256] >> 4], -1).reshape(-1, 16, 32)
+    power = rows[:, 256:272].astype(np.float64)
+    scale = np.where(power == 255, np.nan, 2.0 ** (power - 127))
+    latent = (table[codes] * scale[..., None]).reshape(-1, LATENT_DIM)
+    bits = np.ascontiguousarray(rows[:, 272:]).view(np.uint16)
+    rotated = bits.view(np.float16) if dtype == "fp16" else (bits.astype(np.uint32) << 16).view(np.float32)
+    return np.concatenate([latent, rotated.astype(np.float64)], 1)
+
+
+def axis_rows(rope, positions, axis_of):
+    """[tokens, 64]: angle i's cosine and sine at the token's position on axis_of[i];
+    positions [axes, tokens], clamped into the table."""
+    rope = np.asarray(rope)
+    at = np.clip(np.asarray(positions, np.int64), 0, len(rope) - 1)
+    out = np.empty((at.shape[1], ROPE_DIM), rope.dtype)
+    for i, axis in enumerate(axis_of):
+        out[:, i], out[:, 32 + i] = rope[at[axis], i], rope[at[axis], 32 + i]
+    return out
+
+
+def e4m3_codes(y):
+    """E4M3 codes of float32 values, clamped to +-448 (finite values)."""
+    z = np.clip(np.asarray(y, np.float32), -448, 448)
+    return _nearest_even(np.abs(z), _E4M3).astype(np.uint8) | (np.signbit(z).astype(np.uint8) << 7)
 
 
 def attend_row(q, keys, at, scale, softcap=0.0, slopes=None, position=0, dtype="bf16"):

@@ -31,6 +31,16 @@ Entry points (same names as the C ABI):
   index_k_append(k, positions, slots, rope, kv_pages, k_scales, interleaved)  paged caches:
   index_k_append_mxfp4(k, positions, slots, rope, kv_pages, interleaved)
   latent_append(kv, positions, slots, rope, latent_pages, interleaved)
+  latent_append_mxfp4(kv, positions, slots, rope, latent_pages, interleaved)   4-bit latent rows
+  axis_rotations(positions, axis_map, rope, out)                    rotary positions, several axes:
+  rotate_queries(x, positions, rope, out, axis_map, interleaved)
+  rotate_index_queries(q, positions, rope, codes, axis_map, interleaved)
+  axis_map(axis_of)
+  release_pages(block_table, lens, ended, refs, new_lens, new_refs)        care of the pages:
+  fork_pages(block_table, lens, parents, refs, new_lens, new_refs, src, dst, tokens, counts)
+  compact_pages(block_table, lens, refs, new_table, new_refs, src, dst, counts)
+  copy_pages(caches, src, dst, tokens=None, count=None), PageCaches(caches)
+  pages_workspace_bytes(requests, num_pages)
   paged_attention(q, latent_pages, block_table, row_lens, next_n, scale, out, ...)
   shared_prefix_attention(..., next_n, prefix_pages, scale, out, ...)
   sparse_attention(q, latent_pages, block_table, indices, next_n, scale, out, ...)
@@ -62,7 +72,9 @@ __all__ = [
     "sparse_to_logical", "sparse_topk",
     "topk_workspace_bytes", "topk_rows", "topk_rows_f16", "topk_rows_noalloc", "score_histogram",
     "indexer_status_str", "indexer_time_next_call", "hbm_read_probe", "hbm_read_probe_nt",
-    "hbm_gather_probe", "mfma_valu_probe",
+    "hbm_gather_probe", "mfma_valu_probe", "latent_append_mxfp4", "axis_map", "axis_rotations", "rotate_queries",
+    "rotate_index_queries", "PageCaches", "pages_workspace_bytes", "release_pages", "fork_pages", "compact_pages",
+    "copy_pages",
 ]
 
 KEY_FP32 = 0
@@ -76,6 +88,9 @@ MXFP4_TOKEN_BYTES = 68
 LATENT_DIM = 512
 ROPE_DIM = 64
 LATENT_ROW = 576
+LATENT_MXFP4_ROW = 400
+MAX_AXES = 4
+MAX_CACHES = 1024
 VALUE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 EXPORTED_SYMBOLS = ("indexer_logits", "indexer_logits_f16", "indexer_logits_mxfp4", "block_amax8",
@@ -86,7 +101,9 @@ EXPORTED_SYMBOLS = ("indexer_logits", "indexer_logits_f16", "indexer_logits_mxfp
                     "indexer_time_next_call", "hbm_read_probe", "hbm_read_probe_nt", "hbm_gather_probe",
                     "mfma_valu_probe", "index_k_append", "index_k_append_mxfp4", "latent_append",
                     "attention_workspace_bytes", "shared_prefix_workspace_bytes", "paged_attention",
-                    "shared_prefix_attention", "sparse_attention")
+                    "shared_prefix_attention", "sparse_attention", "latent_append_mxfp4", "axis_rotations",
+                    "rotate_queries", "rotate_index_queries", "pages_workspace_bytes", "release_pages", "fork_pages",
+                    "compact_pages", "copy_pages")
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libpaged_mqa_indexer.so"
@@ -180,6 +197,25 @@ def load_library() -> ctypes.CDLL:
     lib.sparse_attention.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, vp,
                                      vp, vp, vp, sz, vp]
     lib.sparse_attention.restype = ctypes.c_int
+    lib.latent_append_mxfp4.argtypes = lib.latent_append.argtypes
+    lib.latent_append_mxfp4.restype = ctypes.c_int
+    u64 = ctypes.c_uint64
+    lib.axis_rotations.argtypes = [vp, i32, u64, i32, vp, i32, vp, vp]
+    lib.axis_rotations.restype = ctypes.c_int
+    lib.rotate_queries.argtypes = [vp, i64, i64, i32, vp, i32, u64, vp, i32, i32, i32, i32, vp, i64, i64, vp]
+    lib.rotate_queries.restype = ctypes.c_int
+    lib.rotate_index_queries.argtypes = [vp, i64, i64, i32, vp, i32, u64, vp, i32, i32, i32, vp, vp]
+    lib.rotate_index_queries.restype = ctypes.c_int
+    lib.pages_workspace_bytes.argtypes = [i32, i32]
+    lib.pages_workspace_bytes.restype = sz
+    lib.release_pages.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, vp, vp]
+    lib.release_pages.restype = ctypes.c_int
+    lib.fork_pages.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fork_pages.restype = ctypes.c_int
+    lib.compact_pages.argtypes = [vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.compact_pages.restype = ctypes.c_int
+    lib.copy_pages.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i32, vp]
+    lib.copy_pages.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -683,6 +719,233 @@ def latent_append(kv, positions, slots, rope, latent_pages, interleaved=False, e
     _need_shaped(latent_pages, "latent_pages", kv.dtype, kv.device, (latent_pages.shape[0], PAGE_TOKENS, LATENT_ROW))
     _append_call("latent_append", LATENT_ROW, (torch.bfloat16, torch.float16), kv, positions, slots, rope,
                  latent_pages, (), interleaved, events)
+
+
+def latent_append_mxfp4(kv, positions, slots, rope, latent_pages, interleaved=False, events=None):
+    """latent_append into 4-bit rows: latent_pages [P, 64, 400] uint8, per token 256
+    bytes of E2M1 codes, 16 E8M0 bytes (one per 32 dimensions) and the 64 rotated
+    dimensions in kv's type.  A block with a NaN or an infinity becomes NaN."""
+    _need_shaped(latent_pages, "latent_pages", torch.uint8, kv.device,
+                 (latent_pages.shape[0], PAGE_TOKENS, LATENT_MXFP4_ROW))
+    _append_call("latent_append_mxfp4", LATENT_ROW, (torch.bfloat16, torch.float16), kv, positions, slots, rope,
+                 latent_pages, (), interleaved, events)
+
+
+def axis_map(axis_of) -> int:
+    """The axis of each of the 32 angles (a sequence of 32 numbers below 4) as the
+    integer that the rotations take: two bits per angle."""
+    axis_of = [int(a) for a in axis_of]
+    if len(axis_of) != ROPE_DIM // 2 or not all(0 <= a < MAX_AXES for a in axis_of):
+        raise ValueError(f"axis_of must be {ROPE_DIM // 2} axes in 0 .. {MAX_AXES - 1}")
+    return sum(a << (2 * i) for i, a in enumerate(axis_of))
+
+
+def _rotary_positions(positions, rope, dev, tokens):
+    """positions [tokens] or [axes, tokens] -> axes, rows of the table."""
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    _need_shaped(positions, "positions", torch.int32, dev, (tokens,) if positions.dim() == 1 else (axes, tokens))
+    max_positions = rope.shape[0]
+    _need_shaped(rope, "rope", torch.float32, dev, (max_positions, ROPE_DIM))
+    return axes, max_positions
+
+
+def axis_rotations(positions, axis_map, rope, out, events=None):
+    """Each token's cosines and sines of several axes in one row.
+
+    positions [axes, tokens] int32; axis_map as axis_map() gives it; rope
+    [max_positions, 64] float32 as for the appends; out [tokens, 64] float32.  The
+    appends take ``out`` as their table, with positions 0 .. tokens - 1.
+    """
+    dev, tokens = out.device, out.shape[0]
+    _need_shaped(out, "out", torch.float32, dev, (tokens, ROPE_DIM))
+    axes, max_positions = _rotary_positions(positions, rope, dev, tokens)
+    _launch("axis_rotations", dev, events, positions.data_ptr(), axes, axis_map, tokens, rope.data_ptr(),
+            max_positions, out.data_ptr())
+
+
+def _strided_rows(t, name, dtype, dev, shape):
+    """Strides of [tokens, heads, dim] rows; those of a dimension of one element
+    carry no meaning and become those of a packed tensor."""
+    _need(t, name, dtype, dev, 3)
+    if t.shape != shape or t.stride(2) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit stride in the last dimension")
+    tokens, heads, dim = shape
+    token, head = t.stride(0), t.stride(1)
+    if heads == 1:
+        head = dim
+    if tokens == 1:
+        token = heads * max(head, dim)
+    return token, head
+
+
+def rotate_queries(x, positions, rope, out, axis_map=0, interleaved=False, events=None):
+    """Turn the rotated part of every head of every query row by its position.
+
+    x and out [tokens, heads, 64] bfloat16 or float16, any strides with 16-byte
+    rows (such as slices of wider tensors); out may be x itself, otherwise they
+    share no element.  positions [tokens] int32, or [axes, tokens] with
+    ``axis_map``; rope [max_positions, 64] float32; pairs (i, i + 32), or
+    (2i, 2i + 1) with ``interleaved``.
+    """
+    dev, dtype = x.device, x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"x must be bfloat16 or float16, got {dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"x must have 3 dims, got {tuple(x.shape)}")
+    tokens, heads = x.shape[:2]
+    shape = (tokens, heads, ROPE_DIM)
+    strides, out_strides = _strided_rows(x, "x", dtype, dev, shape), _strided_rows(out, "out", dtype, dev, shape)
+    axes, max_positions = _rotary_positions(positions, rope, dev, tokens)
+    _launch("rotate_queries", dev, events, x.data_ptr(), *strides, VALUE_DTYPES[dtype], positions.data_ptr(), axes,
+            axis_map, rope.data_ptr(), max_positions, 1 if interleaved else 0, tokens, heads, out.data_ptr(),
+            *out_strides)
+
+
+def rotate_index_queries(q, positions, rope, codes, axis_map=0, interleaved=False, events=None):
+    """Turn the first 64 of 128 dimensions of the indexer's queries and write all of
+    them as the E4M3 codes that indexer_logits reads.
+
+    q [tokens, 32, 128] bfloat16, float16 or float32 with 16-byte rows; codes
+    [tokens, 32, 128] uint8; other arguments as for rotate_queries.  Values beyond
+    +-448 become +-448.
+    """
+    dev, dtype = q.device, q.dtype
+    if dtype not in VALUE_DTYPES:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+    tokens = q.shape[0]
+    shape = (tokens, HEADS, HEAD_DIM)
+    strides = _strided_rows(q, "q", dtype, dev, shape)
+    _need_shaped(codes, "codes", torch.uint8, dev, shape)
+    axes, max_positions = _rotary_positions(positions, rope, dev, tokens)
+    _launch("rotate_index_queries", dev, events, q.data_ptr(), *strides, VALUE_DTYPES[dtype], positions.data_ptr(),
+            axes, axis_map, rope.data_ptr(), max_positions, 1 if interleaved else 0, tokens, codes.data_ptr())
+
+
+class PageCaches:
+    """The caches that one pool of page ids serves, as copy_pages takes them: GPU
+    tensors [num_pages, 64, ...], contiguous, of the same number of pages (index
+    codes, scales and latent rows of all layers).  Holds on to the tensors."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not 1 <= len(caches) <= MAX_CACHES:
+            raise ValueError(f"1 .. {MAX_CACHES} caches, got {len(caches)}")
+        dev, pages = caches[0].device, caches[0].shape[0]
+        for i, t in enumerate(caches):
+            _need(t, f"caches[{i}]", t.dtype, dev)
+            if t.dim() < 2 or t.shape[0] != pages or t.shape[1] != PAGE_TOKENS or not t.is_contiguous():
+                raise ValueError(f"caches[{i}] must be contiguous [{pages}, {PAGE_TOKENS}, ...], got {tuple(t.shape)}")
+        self.tensors, self.device, self.num_pages = caches, dev, pages
+        self.pointers = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
+        self.token_bytes = (ctypes.c_int32 * len(caches))(*[t[0, 0].numel() * t.element_size() for t in caches])
+
+
+def copy_pages(caches, src, dst, tokens=None, count=None, events=None):
+    """Page src[i] to page dst[i] in every cache (PageCaches, or a list of tensors
+    that becomes one for the call).
+
+    src, dst [n] int32, entries outside the pool (-1) copy nothing; tokens [n] int32:
+    how many of a page's first tokens, or None for all; count int32 [1]: only the
+    first so many entries.  No destination is also a source or given twice.
+    """
+    if not isinstance(caches, PageCaches):
+        caches = PageCaches(caches)
+    dev, n = caches.device, src.shape[0]
+    _need_shaped(src, "src", torch.int32, dev, (n,))
+    _need_shaped(dst, "dst", torch.int32, dev, (n,))
+    if tokens is not None:
+        _need_shaped(tokens, "tokens", torch.int32, dev, (n,))
+    if count is not None:
+        _need_shaped(count, "count", torch.int32, dev, (1,))
+    _launch("copy_pages", dev, events, caches.pointers, caches.token_bytes, len(caches.tensors), caches.num_pages,
+            src.data_ptr(), dst.data_ptr(), _ptr(tokens), _ptr(count), n)
+
+
+def pages_workspace_bytes(requests: int, num_pages: int) -> int:
+    """Workspace of fork_pages and compact_pages."""
+    return int(load_library().pages_workspace_bytes(int(requests), int(num_pages)))
+
+
+def _pool(block_table, lens, refs, **others):
+    """Shapes of a pool: requests, max_pages, num_pages; ``others`` (tensor, "requests"
+    or "pages" or a number of elements)."""
+    dev = block_table.device
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must have 2 dims, got {tuple(block_table.shape)}")
+    requests, max_pages = block_table.shape
+    num_pages = refs.shape[0]
+    _need_shaped(block_table, "block_table", torch.int32, dev, (requests, max_pages))
+    _need_shaped(lens, "lens", torch.int32, dev, (requests,))
+    _need_shaped(refs, "refs", torch.int32, dev, (num_pages,))
+    for name, (t, size) in others.items():
+        size = requests if size == "requests" else num_pages if size == "pages" else size
+        _need_shaped(t, name, torch.int32, dev, (size,))
+    return dev, requests, max_pages, num_pages
+
+
+def _pool_workspace(workspace, requests, num_pages, dev):
+    if workspace is None:
+        return torch.empty(pages_workspace_bytes(requests, num_pages), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def release_pages(block_table, lens, ended, refs, new_lens, new_refs, events=None):
+    """Requests with ended[b] != 0 give up their pages.
+
+    block_table [requests, max_pages] int32, of which request b holds the first
+    ceil(lens[b] / 64) entries; refs [num_pages] int32 holders of each page (0:
+    free); ended [requests] int32.  new_lens and new_refs are written, and may be
+    lens and refs.
+    """
+    dev, requests, max_pages, num_pages = _pool(block_table, lens, refs, ended=(ended, "requests"),
+                                                new_lens=(new_lens, "requests"), new_refs=(new_refs, "pages"))
+    _launch("release_pages", dev, events, block_table.data_ptr(), lens.data_ptr(), ended.data_ptr(), requests,
+            max_pages, refs.data_ptr(), num_pages, new_lens.data_ptr(), new_refs.data_ptr())
+
+
+def fork_pages(block_table, lens, parents, refs, new_lens, new_refs, src, dst, tokens, counts, workspace=None,
+               events=None):
+    """Request b without tokens becomes a copy of request parents[b] (negative: none).
+
+    It shares the full pages; the page that the parent has begun is to be copied to
+    the lowest free one: src, dst, tokens [requests] int32 name the copies as
+    copy_pages takes them (-1, -1, 0: none).  Rows of block_table are written for
+    the forked requests; new_lens and new_refs may be lens and refs.  counts [2]
+    int32: pages taken, and requests not forked because none was left.
+    ``workspace``: pages_workspace_bytes(requests, num_pages) bytes, allocated for
+    the call when None.
+    """
+    dev, requests, max_pages, num_pages = _pool(
+        block_table, lens, refs, parents=(parents, "requests"), new_lens=(new_lens, "requests"),
+        new_refs=(new_refs, "pages"), src=(src, "requests"), dst=(dst, "requests"), tokens=(tokens, "requests"),
+        counts=(counts, 2))
+    workspace = _pool_workspace(workspace, requests, num_pages, dev)
+    _launch("fork_pages", dev, events, block_table.data_ptr(), lens.data_ptr(), parents.data_ptr(), requests,
+            max_pages, refs.data_ptr(), num_pages, new_lens.data_ptr(), new_refs.data_ptr(), src.data_ptr(),
+            dst.data_ptr(), tokens.data_ptr(), counts.data_ptr(), workspace.data_ptr(), workspace.numel())
+
+
+def compact_pages(block_table, lens, refs, new_table, new_refs, src, dst, counts, workspace=None, events=None):
+    """Plan the moves that make the pool dense: with L pages held, the held pages from
+    L on go to the free ones below L.
+
+    src and dst [num_pages] int32 name the moves (-1 behind the last), counts [2]
+    int32 is L and their number: copy_pages(caches, src, dst, count=counts[1:]).
+    new_table [requests, max_pages] and new_refs [num_pages] say where the pages
+    then are, and may be block_table and refs.
+    """
+    dev, requests, max_pages, num_pages = _pool(block_table, lens, refs, new_refs=(new_refs, "pages"),
+                                                src=(src, "pages"), dst=(dst, "pages"), counts=(counts, 2))
+    _need_shaped(new_table, "new_table", torch.int32, dev, (requests, max_pages))
+    workspace = _pool_workspace(workspace, requests, num_pages, dev)
+    _launch("compact_pages", dev, events, block_table.data_ptr(), lens.data_ptr(), requests, max_pages,
+            refs.data_ptr(), num_pages, new_table.data_ptr(), new_refs.data_ptr(), src.data_ptr(), dst.data_ptr(),
+            counts.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def attention_workspace_bytes(rows: int, heads: int, requests: int) -> int:

@@ -344,7 +344,7 @@ idx_status sparse_topk(const float* scores, int64_t stride, const int32_t* hist,
 static idx_status append_call(const void* rows, int64_t row_stride, int32_t row_dim, int32_t dtype,
                               const int32_t* positions, const int32_t* slots, const float* rope,
                               int32_t max_positions, int32_t interleaved, int32_t tokens, int32_t num_pages,
-                              void* pages, float* k_scales, bool latent, void* stream) {
+                              void* pages, float* k_scales, bool latent, bool mxfp4_rows, void* stream) {
   const pmqa::LaunchEvents ev = take_events();
   if (!rows || !positions || !slots || !rope || !pages) return IDX_EINVAL;
   if (tokens <= 0 || num_pages <= 0 || max_positions <= 0 || row_stride < row_dim) return IDX_EINVAL;
@@ -369,7 +369,7 @@ static idx_status append_call(const void* rows, int64_t row_stride, int32_t row_
   a.tokens = tokens;
   a.num_pages = num_pages;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return from_hip(latent ? pmqa::launch_latent_append(a, s, ev) : pmqa::launch_index_k_append(a, s, ev));
+  return from_hip(latent ? pmqa::launch_latent_append(a, mxfp4_rows, s, ev) : pmqa::launch_index_k_append(a, s, ev));
 }
 
 idx_status index_k_append(const void* k, int64_t k_stride, int32_t k_dtype, const int32_t* positions,
@@ -380,21 +380,235 @@ idx_status index_k_append(const void* k, int64_t k_stride, int32_t k_dtype, cons
     return IDX_EINVAL;
   }
   return append_call(k, k_stride, IDX_HEAD_DIM, k_dtype, positions, slots, rope, max_positions, interleaved, tokens,
-                     num_pages, kv_pages, k_scales, false, stream);
+                     num_pages, kv_pages, k_scales, false, false, stream);
 }
 
 idx_status index_k_append_mxfp4(const void* k, int64_t k_stride, int32_t k_dtype, const int32_t* positions,
                                 const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
                                 int32_t tokens, int32_t num_pages, uint8_t* kv_pages, void* stream) {
   return append_call(k, k_stride, IDX_HEAD_DIM, k_dtype, positions, slots, rope, max_positions, interleaved, tokens,
-                     num_pages, kv_pages, nullptr, false, stream);
+                     num_pages, kv_pages, nullptr, false, false, stream);
 }
 
 idx_status latent_append(const void* kv, int64_t kv_stride, int32_t dtype, const int32_t* positions,
                          const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
                          int32_t tokens, int32_t num_pages, void* latent_pages, void* stream) {
   return append_call(kv, kv_stride, IDX_LATENT_ROW, dtype, positions, slots, rope, max_positions, interleaved, tokens,
-                     num_pages, latent_pages, nullptr, true, stream);
+                     num_pages, latent_pages, nullptr, true, false, stream);
+}
+
+idx_status latent_append_mxfp4(const void* kv, int64_t kv_stride, int32_t dtype, const int32_t* positions,
+                               const int32_t* slots, const float* rope, int32_t max_positions, int32_t interleaved,
+                               int32_t tokens, int32_t num_pages, uint8_t* latent_pages, void* stream) {
+  return append_call(kv, kv_stride, IDX_LATENT_ROW, dtype, positions, slots, rope, max_positions, interleaved, tokens,
+                     num_pages, latent_pages, nullptr, true, true, stream);
+}
+
+// What the rotations have in common.
+static idx_status check_rotary(const pmqa::RotaryArgs& a) {
+  if (!a.positions || !a.rope || !a.out) return IDX_EINVAL;
+  if (a.tokens <= 0 || a.max_positions <= 0) return IDX_EINVAL;
+  if (a.axes < 1 || a.axes > IDX_MAX_AXES) return IDX_EINVAL;
+  for (int i = 0; i < IDX_ROPE_DIM / 2; ++i)
+    if (static_cast<int>(a.axis_map >> (2 * i) & 3) >= a.axes) return IDX_EINVAL;
+  if (a.tokens > IDX_MAX_APPEND_TOKENS) return IDX_EUNSUPPORTED;
+  if (!aligned(a.positions, 4) || !aligned(a.rope, 16) || !aligned(a.out, 16)) return IDX_EALIGN;
+  return IDX_OK;
+}
+
+// [tokens][heads] rows of `dim` elements whose last byte is within 63 bits.
+static idx_status check_rows(const void* p, int64_t token_stride, int64_t head_stride, int32_t tokens, int32_t heads,
+                             int64_t per16) {
+  if (token_stride < 0 || head_stride < 0) return IDX_EINVAL;
+  if (token_stride > INT64_MAX / 8 / tokens || head_stride > INT64_MAX / 8 / heads) return IDX_EUNSUPPORTED;
+  if (!aligned(p, 16) || token_stride % per16 != 0 || head_stride % per16 != 0) return IDX_EALIGN;
+  return IDX_OK;
+}
+
+idx_status axis_rotations(const int32_t* positions, int32_t axes, uint64_t axis_map, int32_t tokens, const float* rope,
+                          int32_t max_positions, float* out, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  pmqa::RotaryArgs a{};
+  a.positions = positions;
+  a.axes = axes;
+  a.axis_map = axis_map;
+  a.tokens = tokens;
+  a.rope = rope;
+  a.max_positions = max_positions;
+  a.out = out;
+  const idx_status st = check_rotary(a);
+  if (st != IDX_OK) return st;
+  return from_hip(pmqa::launch_axis_rotations(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status rotate_queries(const void* x, int64_t x_token_stride, int64_t x_head_stride, int32_t dtype,
+                          const int32_t* positions, int32_t axes, uint64_t axis_map, const float* rope,
+                          int32_t max_positions, int32_t interleaved, int32_t tokens, int32_t heads, void* out,
+                          int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  pmqa::RotaryArgs a{x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, positions, rope,
+                     axis_map, axes, dtype, max_positions, interleaved, tokens, heads};
+  idx_status st = check_rotary(a);
+  if (!x || heads <= 0) return IDX_EINVAL;
+  if (st != IDX_OK) return st;
+  if (dtype != IDX_BF16 && dtype != IDX_FP16) return IDX_EUNSUPPORTED;
+  if (heads > IDX_MAX_ATTENTION_HEADS) return IDX_EUNSUPPORTED;
+  if ((st = check_rows(x, x_token_stride, x_head_stride, tokens, heads, 8)) != IDX_OK) return st;
+  if ((st = check_rows(out, out_token_stride, out_head_stride, tokens, heads, 8)) != IDX_OK) return st;
+  // the rows written lie apart: heads within tokens or tokens within heads
+  const int64_t last_head = (heads - 1) * out_head_stride, last_token = (tokens - 1) * out_token_stride;
+  const bool heads_apart = heads == 1 || out_head_stride >= IDX_ROPE_DIM;
+  const bool tokens_apart = tokens == 1 || out_token_stride >= IDX_ROPE_DIM;
+  const bool nested = tokens == 1 || heads == 1 || out_token_stride >= last_head + IDX_ROPE_DIM ||
+                      out_head_stride >= last_token + IDX_ROPE_DIM;
+  if (!heads_apart || !tokens_apart || !nested) return IDX_EINVAL;
+  // in place: every row onto itself
+  if (x == out && ((heads > 1 && x_head_stride != out_head_stride) || (tokens > 1 && x_token_stride != out_token_stride)))
+    return IDX_EINVAL;
+  return from_hip(pmqa::launch_rotate_queries(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status rotate_index_queries(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t dtype,
+                                const int32_t* positions, int32_t axes, uint64_t axis_map, const float* rope,
+                                int32_t max_positions, int32_t interleaved, int32_t tokens, uint8_t* codes,
+                                void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  pmqa::RotaryArgs a{q, q_token_stride, q_head_stride, codes, IDX_NUM_HEADS * IDX_HEAD_DIM, IDX_HEAD_DIM, positions,
+                     rope, axis_map, axes, dtype, max_positions, interleaved, tokens, IDX_NUM_HEADS};
+  idx_status st = check_rotary(a);
+  if (!q) return IDX_EINVAL;
+  if (st != IDX_OK) return st;
+  if (dtype != IDX_BF16 && dtype != IDX_FP16 && dtype != IDX_FP32) return IDX_EUNSUPPORTED;
+  if ((st = check_rows(q, q_token_stride, q_head_stride, tokens, IDX_NUM_HEADS, dtype == IDX_FP32 ? 4 : 8)) != IDX_OK)
+    return st;
+  return from_hip(pmqa::launch_rotate_index_queries(a, static_cast<hipStream_t>(stream), ev));
+}
+
+static bool pool_sizes_ok(int32_t requests, int32_t max_pages, int32_t num_pages) {
+  return requests <= IDX_MAX_REQUESTS && num_pages <= IDX_MAX_CACHE_PAGES && max_pages <= IDX_MAX_ATTENTION_PAGES &&
+         static_cast<int64_t>(requests) * max_pages <= INT32_MAX;
+}
+
+size_t pages_workspace_bytes(int32_t requests, int32_t num_pages) {
+  return pmqa::pages_workspace_size(requests, num_pages);
+}
+
+idx_status release_pages(const int32_t* block_table, const int32_t* lens, const int32_t* ended, int32_t requests,
+                         int32_t max_pages, const int32_t* refs, int32_t num_pages, int32_t* new_lens,
+                         int32_t* new_refs, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  if (!block_table || !lens || !ended || !refs || !new_lens || !new_refs) return IDX_EINVAL;
+  if (requests <= 0 || max_pages <= 0 || num_pages <= 0) return IDX_EINVAL;
+  if (!pool_sizes_ok(requests, max_pages, num_pages)) return IDX_EUNSUPPORTED;
+  if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(ended, 4) || !aligned(refs, 4) ||
+      !aligned(new_lens, 4) || !aligned(new_refs, 4))
+    return IDX_EALIGN;
+  pmqa::PageArgs a{};
+  a.block_table = const_cast<int32_t*>(block_table);  // only read
+  a.lens = lens;
+  a.mask = ended;
+  a.refs = refs;
+  a.new_lens = new_lens;
+  a.new_refs = new_refs;
+  a.requests = requests;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  return from_hip(pmqa::launch_release_pages(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status fork_pages(int32_t* block_table, const int32_t* lens, const int32_t* parents, int32_t requests,
+                      int32_t max_pages, const int32_t* refs, int32_t num_pages, int32_t* new_lens, int32_t* new_refs,
+                      int32_t* src, int32_t* dst, int32_t* tokens, int32_t* counts, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  if (!block_table || !lens || !parents || !refs || !new_lens || !new_refs || !src || !dst || !tokens || !counts ||
+      !workspace)
+    return IDX_EINVAL;
+  if (requests <= 0 || max_pages <= 0 || num_pages <= 0) return IDX_EINVAL;
+  if (!pool_sizes_ok(requests, max_pages, num_pages)) return IDX_EUNSUPPORTED;
+  if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(parents, 4) || !aligned(refs, 4) ||
+      !aligned(new_lens, 4) || !aligned(new_refs, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4) ||
+      !aligned(counts, 4) || !aligned(workspace, 256))
+    return IDX_EALIGN;
+  if (workspace_bytes < pmqa::pages_workspace_size(requests, num_pages)) return IDX_EWORKSPACE;
+  pmqa::PageArgs a{};
+  a.block_table = block_table;
+  a.lens = lens;
+  a.mask = parents;
+  a.refs = refs;
+  a.new_lens = new_lens;
+  a.new_refs = new_refs;
+  a.src = src;
+  a.dst = dst;
+  a.tokens = tokens;
+  a.counts = counts;
+  a.workspace = workspace;
+  a.requests = requests;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  return from_hip(pmqa::launch_fork_pages(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status compact_pages(const int32_t* block_table, const int32_t* lens, int32_t requests, int32_t max_pages,
+                         const int32_t* refs, int32_t num_pages, int32_t* new_table, int32_t* new_refs, int32_t* src,
+                         int32_t* dst, int32_t* counts, void* workspace, size_t workspace_bytes, void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  if (!block_table || !lens || !refs || !new_table || !new_refs || !src || !dst || !counts || !workspace)
+    return IDX_EINVAL;
+  if (requests <= 0 || max_pages <= 0 || num_pages <= 0) return IDX_EINVAL;
+  if (!pool_sizes_ok(requests, max_pages, num_pages)) return IDX_EUNSUPPORTED;
+  if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(refs, 4) || !aligned(new_table, 4) ||
+      !aligned(new_refs, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(counts, 4) || !aligned(workspace, 256))
+    return IDX_EALIGN;
+  if (workspace_bytes < pmqa::pages_workspace_size(requests, num_pages)) return IDX_EWORKSPACE;
+  pmqa::PageArgs a{};
+  a.block_table = const_cast<int32_t*>(block_table);  // only read
+  a.lens = lens;
+  a.refs = refs;
+  a.new_table = new_table;
+  a.new_refs = new_refs;
+  a.src = src;
+  a.dst = dst;
+  a.counts = counts;
+  a.workspace = workspace;
+  a.requests = requests;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  return from_hip(pmqa::launch_compact_pages(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status copy_pages(void* const* caches, const int32_t* token_bytes, int32_t n_caches, int32_t num_pages,
+                      const int32_t* src, const int32_t* dst, const int32_t* tokens, const int32_t* count, int32_t n,
+                      void* stream) {
+  const pmqa::LaunchEvents ev = take_events();
+  if (!caches || !token_bytes || !src || !dst) return IDX_EINVAL;
+  if (n_caches <= 0 || num_pages <= 0 || n <= 0) return IDX_EINVAL;
+  if (n_caches > IDX_MAX_CACHES || num_pages > IDX_MAX_CACHE_PAGES || n > IDX_MAX_CACHE_PAGES) return IDX_EUNSUPPORTED;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4) || !aligned(count, 4)) return IDX_EALIGN;
+  for (int32_t i = 0; i < n_caches; ++i) {
+    if (!caches[i] || token_bytes[i] <= 0) return IDX_EINVAL;
+    if (token_bytes[i] > IDX_MAX_TOKEN_BYTES) return IDX_EUNSUPPORTED;
+    if (!aligned(caches[i], 16) || token_bytes[i] % 4 != 0) return IDX_EALIGN;
+  }
+  for (int32_t first = 0; first < n_caches; first += pmqa::kCopyCaches) {
+    pmqa::CopyArgs a{};
+    a.caches = n_caches - first < pmqa::kCopyCaches ? n_caches - first : pmqa::kCopyCaches;
+    for (int32_t i = 0; i < a.caches; ++i) {
+      a.base[i] = caches[first + i];
+      a.token_bytes[i] = token_bytes[first + i];
+    }
+    a.src = src;
+    a.dst = dst;
+    a.tokens = tokens;
+    a.count = count;
+    a.n = n;
+    a.num_pages = num_pages;
+    const bool last = first + a.caches == n_caches;
+    const hipError_t e = pmqa::launch_copy_pages(a, static_cast<hipStream_t>(stream), first == 0 ? ev.start : nullptr,
+                                                 last ? ev.stop : nullptr);
+    if (e != hipSuccess) return from_hip(e);
+  }
+  return IDX_OK;
 }
 
 // What the three attention calls have in common; `keys` is row_lens or indices.

@@ -240,7 +240,60 @@ struct AppendArgs {
   int32_t num_pages;
 };
 
-// Attention over the latent cache [num_pages][64][576].
+// Rotation of queries, and the composition of several axes' rotations.
+struct RotaryArgs {
+  const void* x;             // [tokens][heads] rows, strides in elements
+  int64_t x_token_stride;
+  int64_t x_head_stride;
+  void* out;
+  int64_t out_token_stride;
+  int64_t out_head_stride;
+  const int32_t* positions;  // [axes][tokens]
+  const float* rope;         // [max_positions][64]
+  uint64_t axis_map;         // two bits per angle: its axis
+  int32_t axes;
+  int32_t dtype;
+  int32_t max_positions;
+  int32_t interleaved;
+  int32_t tokens;
+  int32_t heads;
+};
+
+// Release, fork and compaction of the pages of a pool.
+struct PageArgs {
+  int32_t* block_table;   // [requests][max_pages] (written by a fork only)
+  const int32_t* lens;    // [requests] tokens
+  const int32_t* mask;    // [requests] release: nonzero ends; fork: the parent, or negative
+  const int32_t* refs;    // [num_pages]
+  int32_t* new_table;     // [requests][max_pages] (compact)
+  int32_t* new_lens;      // [requests]
+  int32_t* new_refs;      // [num_pages]
+  int32_t* src;           // [requests] (fork) or [num_pages] (compact)
+  int32_t* dst;
+  int32_t* tokens;        // [requests] (fork)
+  int32_t* counts;        // [2]
+  void* workspace;
+  int32_t requests;
+  int32_t max_pages;
+  int32_t num_pages;
+};
+
+// Copies of pages in up to kCopyCaches caches.
+constexpr int kCopyCaches = 128;
+struct CopyArgs {
+  void* base[kCopyCaches];
+  int32_t token_bytes[kCopyCaches];
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* tokens;  // or null: whole pages
+  const int32_t* count;   // or null: n
+  int32_t caches;
+  int32_t n;
+  int32_t num_pages;
+};
+
+// Attention over the latent cache [num_pages][64][576], or [num_pages][64][400]
+// bytes of 4-bit rows.
 struct AttentionArgs {
   const void* q;                 // [rows][heads][576]
   const void* cache;

@@ -53,7 +53,17 @@ hipError_t launch_mfma_valu_probe(int mode, int workgroups, int iters, float* ou
                                   LaunchEvents ev = {});
 
 hipError_t launch_index_k_append(const AppendArgs& a, hipStream_t stream, LaunchEvents ev = {});
-hipError_t launch_latent_append(const AppendArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_latent_append(const AppendArgs& a, bool mxfp4, hipStream_t stream, LaunchEvents ev = {});
+
+hipError_t launch_axis_rotations(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_rotate_queries(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_rotate_index_queries(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev = {});
+
+size_t pages_workspace_size(int32_t requests, int32_t num_pages);
+hipError_t launch_release_pages(const PageArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_fork_pages(const PageArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_compact_pages(const PageArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_copy_pages(const CopyArgs& a, hipStream_t stream, hipEvent_t start, hipEvent_t stop);
 
 size_t attention_workspace_size(int32_t rows, int32_t heads, int32_t requests);
 size_t shared_prefix_workspace_size(int32_t rows, int32_t heads, int32_t requests);
