@@ -768,6 +768,40 @@ idx_status sparse_attention(const void* q, const void* latent_pages, int32_t dty
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * paged_attention_mxfp4, shared_prefix_attention_mxfp4, sparse_attention_mxfp4 -- the
+ * same over the 4-bit latent cache (IDX_LATENT_MXFP4_ROW, as latent_append_mxfp4
+ * writes it): a key's values are its codes times their blocks' powers of two, taken
+ * in q's type, in which what was appended from rows of that type is exact (foreign
+ * powers of two may leave its range: infinities, and rounded values below), and the
+ * rotated part, which holds q's type.  Results are those of the calls above over a
+ * cache of these values, with the same masks, NaN and infinities, arguments and
+ * workspaces.
+ *
+ * latent_pages (device) uint8 [num_pages][64][400], 16-B aligned
+ * dtype        of q, out and the rotated part: BF16 or FP16
+ */
+idx_status paged_attention_mxfp4(const void* q, const uint8_t* latent_pages, int32_t dtype, const int32_t* block_table,
+                                 const int32_t* row_lens, const int32_t* row_starts, const int32_t* cu_q, int32_t rows,
+                                 int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages,
+                                 float scale, float softcap, const float* slopes, const int32_t* row_positions,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+idx_status shared_prefix_attention_mxfp4(const void* q, const uint8_t* latent_pages, int32_t dtype,
+                                         const int32_t* block_table, const int32_t* row_lens,
+                                         const int32_t* row_starts, int32_t rows, int32_t heads, int32_t requests,
+                                         int32_t next_n, int32_t prefix_pages, int32_t num_pages, int32_t max_pages,
+                                         float scale, float softcap, const float* slopes, const int32_t* row_positions,
+                                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+idx_status sparse_attention_mxfp4(const void* q, const uint8_t* latent_pages, int32_t dtype,
+                                  const int32_t* block_table, const int32_t* indices, int32_t k, const int32_t* cu_q,
+                                  int32_t rows, int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages,
+                                  int32_t max_pages, float scale, float softcap, const float* slopes,
+                                  const int32_t* row_positions, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
  * indexer_time_next_call -- measurement aid.  Arms the calling host thread:
  * its next call of this library records start_event when that call's first
  * kernel begins and stop_event when its last kernel ends (the dispatches

@@ -44,6 +44,7 @@ Entry points (same names as the C ABI):
   paged_attention(q, latent_pages, block_table, row_lens, next_n, scale, out, ...)
   shared_prefix_attention(..., next_n, prefix_pages, scale, out, ...)
   sparse_attention(q, latent_pages, block_table, indices, next_n, scale, out, ...)
+  paged_attention_mxfp4, shared_prefix_attention_mxfp4, sparse_attention_mxfp4: the same over 4-bit rows
   attention_workspace_bytes(rows, heads, requests), shared_prefix_workspace_bytes(...)
   indexer_status_str(status)
   indexer_time_next_call(start, stop)
@@ -74,7 +75,7 @@ __all__ = [
     "indexer_status_str", "indexer_time_next_call", "hbm_read_probe", "hbm_read_probe_nt",
     "hbm_gather_probe", "mfma_valu_probe", "latent_append_mxfp4", "axis_map", "axis_rotations", "rotate_queries",
     "rotate_index_queries", "PageCaches", "pages_workspace_bytes", "release_pages", "fork_pages", "compact_pages",
-    "copy_pages",
+    "copy_pages", "paged_attention_mxfp4", "shared_prefix_attention_mxfp4", "sparse_attention_mxfp4",
 ]
 
 KEY_FP32 = 0
@@ -103,7 +104,8 @@ EXPORTED_SYMBOLS = ("indexer_logits", "indexer_logits_f16", "indexer_logits_mxfp
                     "attention_workspace_bytes", "shared_prefix_workspace_bytes", "paged_attention",
                     "shared_prefix_attention", "sparse_attention", "latent_append_mxfp4", "axis_rotations",
                     "rotate_queries", "rotate_index_queries", "pages_workspace_bytes", "release_pages", "fork_pages",
-                    "compact_pages", "copy_pages")
+                    "compact_pages", "copy_pages", "paged_attention_mxfp4", "shared_prefix_attention_mxfp4",
+                    "sparse_attention_mxfp4")
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libpaged_mqa_indexer.so"
@@ -197,6 +199,9 @@ def load_library() -> ctypes.CDLL:
     lib.sparse_attention.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, vp,
                                      vp, vp, vp, sz, vp]
     lib.sparse_attention.restype = ctypes.c_int
+    for name in ("paged_attention", "shared_prefix_attention", "sparse_attention"):
+        getattr(lib, name + "_mxfp4").argtypes = getattr(lib, name).argtypes
+        getattr(lib, name + "_mxfp4").restype = ctypes.c_int
     lib.latent_append_mxfp4.argtypes = lib.latent_append.argtypes
     lib.latent_append_mxfp4.restype = ctypes.c_int
     u64 = ctypes.c_uint64
@@ -959,7 +964,8 @@ def shared_prefix_workspace_bytes(rows: int, heads: int, requests: int) -> int:
 
 def _attention_call(name, q, latent_pages, block_table, keys, next_n, cu_q, starts, prefix_pages, scale, out, lse,
                     softcap, slopes, row_positions, workspace, events):
-    """keys: row_lens [rows], or the selected keys [rows, k] (sparse_attention)."""
+    """keys: row_lens [rows], or the selected keys [rows, k] (sparse_attention).
+    The _mxfp4 entry points take the cache in 4-bit rows."""
     dev, dtype = q.device, q.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
@@ -968,12 +974,15 @@ def _attention_call(name, q, latent_pages, block_table, keys, next_n, cu_q, star
     rows, heads = q.shape[:2]
     _need_shaped(q, "q", dtype, dev, (rows, heads, LATENT_ROW))
     pages = latent_pages.shape[0]
-    _need_shaped(latent_pages, "latent_pages", dtype, dev, (pages, PAGE_TOKENS, LATENT_ROW))
+    if name.endswith("_mxfp4"):
+        _need_shaped(latent_pages, "latent_pages", torch.uint8, dev, (pages, PAGE_TOKENS, LATENT_MXFP4_ROW))
+    else:
+        _need_shaped(latent_pages, "latent_pages", dtype, dev, (pages, PAGE_TOKENS, LATENT_ROW))
     if block_table.dim() != 2:
         raise ValueError(f"block_table must have 2 dims, got {tuple(block_table.shape)}")
     requests, max_pages = block_table.shape
     _need_shaped(block_table, "block_table", torch.int32, dev, (requests, max_pages))
-    sparse = name == "sparse_attention"
+    sparse = name.startswith("sparse_attention")
     if sparse:
         _need_shaped(keys, "indices", torch.int32, dev, (rows, keys.shape[-1]))
     else:
@@ -1053,6 +1062,29 @@ def sparse_attention(q, latent_pages, block_table, indices, next_n, scale, out, 
     Other arguments as for paged_attention; slopes need row_positions."""
     _attention_call("sparse_attention", q, latent_pages, block_table, indices, next_n, cu_q, None, None, scale, out,
                     lse, softcap, slopes, row_positions, workspace, events)
+
+
+def paged_attention_mxfp4(q, latent_pages, block_table, row_lens, next_n, scale, out, lse=None, cu_q=None,
+                          row_starts=None, softcap=0.0, slopes=None, row_positions=None, workspace=None, events=None):
+    """paged_attention over the 4-bit latent cache: latent_pages [P, 64, 400] uint8 as
+    latent_append_mxfp4 writes it, from rows of q's type."""
+    _attention_call("paged_attention_mxfp4", q, latent_pages, block_table, row_lens, next_n, cu_q, row_starts, None,
+                    scale, out, lse, softcap, slopes, row_positions, workspace, events)
+
+
+def shared_prefix_attention_mxfp4(q, latent_pages, block_table, row_lens, next_n, prefix_pages, scale, out, lse=None,
+                                  row_starts=None, softcap=0.0, slopes=None, row_positions=None, workspace=None,
+                                  events=None):
+    """shared_prefix_attention over the 4-bit latent cache [P, 64, 400] uint8."""
+    _attention_call("shared_prefix_attention_mxfp4", q, latent_pages, block_table, row_lens, next_n, None, row_starts,
+                    prefix_pages, scale, out, lse, softcap, slopes, row_positions, workspace, events)
+
+
+def sparse_attention_mxfp4(q, latent_pages, block_table, indices, next_n, scale, out, lse=None, cu_q=None,
+                           softcap=0.0, slopes=None, row_positions=None, workspace=None, events=None):
+    """sparse_attention over the 4-bit latent cache [P, 64, 400] uint8."""
+    _attention_call("sparse_attention_mxfp4", q, latent_pages, block_table, indices, next_n, cu_q, None, None, scale,
+                    out, lse, softcap, slopes, row_positions, workspace, events)
 
 
 def _read_probe(name: str, src: torch.Tensor, sink: torch.Tensor, events) -> None:

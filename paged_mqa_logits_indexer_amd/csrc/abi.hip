@@ -611,7 +611,11 @@ idx_status copy_pages(void* const* caches, const int32_t* token_bytes, int32_t n
   return IDX_OK;
 }
 
-// What the three attention calls have in common; `keys` is row_lens or indices.
+// The attention calls come in pairs, over 16-bit and over 4-bit rows, which differ in
+// what is launched.
+using AttentionLaunch = hipError_t(const pmqa::AttentionArgs&, hipStream_t, pmqa::LaunchEvents);
+
+// What they have in common; `keys` is row_lens or indices.
 static idx_status check_attention(const pmqa::AttentionArgs& a, const void* keys, size_t workspace_bytes, size_t need) {
   if (!a.q || !a.cache || !a.block_table || !keys || !a.out || !a.workspace) return IDX_EINVAL;
   if (a.rows <= 0 || a.heads <= 0 || a.requests <= 0 || a.num_pages <= 0 || a.max_pages <= 0 || a.next_n < 0)
@@ -669,11 +673,12 @@ static pmqa::AttentionArgs attention_args(const void* q, const void* latent_page
   return a;
 }
 
-idx_status paged_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
-                           const int32_t* row_lens, const int32_t* row_starts, const int32_t* cu_q, int32_t rows,
-                           int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages,
-                           float scale, float softcap, const float* slopes, const int32_t* row_positions, void* out,
-                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+static idx_status paged_attention_call(AttentionLaunch* launch, const void* q, const void* latent_pages, int32_t dtype,
+                                       const int32_t* block_table, const int32_t* row_lens, const int32_t* row_starts,
+                                       const int32_t* cu_q, int32_t rows, int32_t heads, int32_t requests,
+                                       int32_t next_n, int32_t num_pages, int32_t max_pages, float scale,
+                                       float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   const pmqa::LaunchEvents ev = take_events();
   pmqa::AttentionArgs a = attention_args(q, latent_pages, dtype, block_table, cu_q, rows, heads, requests, next_n,
                                          num_pages, max_pages, scale, softcap, slopes, row_positions, out, lse,
@@ -683,15 +688,36 @@ idx_status paged_attention(const void* q, const void* latent_pages, int32_t dtyp
   const idx_status st = check_attention(a, row_lens, workspace_bytes,
                                         pmqa::attention_workspace_size(rows, heads, requests));
   if (st != IDX_OK) return st;
-  return from_hip(pmqa::launch_paged_attention(a, static_cast<hipStream_t>(stream), ev));
+  return from_hip(launch(a, static_cast<hipStream_t>(stream), ev));
 }
 
-idx_status shared_prefix_attention(const void* q, const void* latent_pages, int32_t dtype,
-                                   const int32_t* block_table, const int32_t* row_lens, const int32_t* row_starts,
-                                   int32_t rows, int32_t heads, int32_t requests, int32_t next_n,
-                                   int32_t prefix_pages, int32_t num_pages, int32_t max_pages, float scale,
-                                   float softcap, const float* slopes, const int32_t* row_positions, void* out,
-                                   float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+idx_status paged_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                           const int32_t* row_lens, const int32_t* row_starts, const int32_t* cu_q, int32_t rows,
+                           int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages,
+                           float scale, float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_attention_call(pmqa::launch_paged_attention, q, latent_pages, dtype, block_table, row_lens, row_starts,
+                              cu_q, rows, heads, requests, next_n, num_pages, max_pages, scale, softcap, slopes,
+                              row_positions, out, lse, workspace, workspace_bytes, stream);
+}
+
+idx_status paged_attention_mxfp4(const void* q, const uint8_t* latent_pages, int32_t dtype, const int32_t* block_table,
+                                 const int32_t* row_lens, const int32_t* row_starts, const int32_t* cu_q, int32_t rows,
+                                 int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages,
+                                 float scale, float softcap, const float* slopes, const int32_t* row_positions,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_attention_call(pmqa::launch_paged_attention_mxfp4, q, latent_pages, dtype, block_table, row_lens,
+                              row_starts, cu_q, rows, heads, requests, next_n, num_pages, max_pages, scale, softcap,
+                              slopes, row_positions, out, lse, workspace, workspace_bytes, stream);
+}
+
+static idx_status shared_prefix_attention_call(AttentionLaunch* launch, const void* q, const void* latent_pages,
+                                               int32_t dtype, const int32_t* block_table, const int32_t* row_lens,
+                                               const int32_t* row_starts, int32_t rows, int32_t heads,
+                                               int32_t requests, int32_t next_n, int32_t prefix_pages,
+                                               int32_t num_pages, int32_t max_pages, float scale, float softcap,
+                                               const float* slopes, const int32_t* row_positions, void* out,
+                                               float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   const pmqa::LaunchEvents ev = take_events();
   pmqa::AttentionArgs a = attention_args(q, latent_pages, dtype, block_table, nullptr, rows, heads, requests, next_n,
                                          num_pages, max_pages, scale, softcap, slopes, row_positions, out, lse,
@@ -703,14 +729,40 @@ idx_status shared_prefix_attention(const void* q, const void* latent_pages, int3
   const idx_status st = check_attention(a, row_lens, workspace_bytes,
                                         pmqa::shared_prefix_workspace_size(rows, heads, requests));
   if (st != IDX_OK) return st;
-  return from_hip(pmqa::launch_shared_prefix_attention(a, static_cast<hipStream_t>(stream), ev));
+  return from_hip(launch(a, static_cast<hipStream_t>(stream), ev));
 }
 
-idx_status sparse_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
-                            const int32_t* indices, int32_t k, const int32_t* cu_q, int32_t rows, int32_t heads,
-                            int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages, float scale,
-                            float softcap, const float* slopes, const int32_t* row_positions, void* out, float* lse,
-                            void* workspace, size_t workspace_bytes, void* stream) {
+idx_status shared_prefix_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                                   const int32_t* row_lens, const int32_t* row_starts, int32_t rows, int32_t heads,
+                                   int32_t requests, int32_t next_n, int32_t prefix_pages, int32_t num_pages,
+                                   int32_t max_pages, float scale, float softcap, const float* slopes,
+                                   const int32_t* row_positions, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return shared_prefix_attention_call(pmqa::launch_shared_prefix_attention, q, latent_pages, dtype, block_table,
+                                      row_lens, row_starts, rows, heads, requests, next_n, prefix_pages, num_pages,
+                                      max_pages, scale, softcap, slopes, row_positions, out, lse, workspace,
+                                      workspace_bytes, stream);
+}
+
+idx_status shared_prefix_attention_mxfp4(const void* q, const uint8_t* latent_pages, int32_t dtype,
+                                         const int32_t* block_table, const int32_t* row_lens,
+                                         const int32_t* row_starts, int32_t rows, int32_t heads, int32_t requests,
+                                         int32_t next_n, int32_t prefix_pages, int32_t num_pages, int32_t max_pages,
+                                         float scale, float softcap, const float* slopes, const int32_t* row_positions,
+                                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+  return shared_prefix_attention_call(pmqa::launch_shared_prefix_attention_mxfp4, q, latent_pages, dtype, block_table,
+                                      row_lens, row_starts, rows, heads, requests, next_n, prefix_pages, num_pages,
+                                      max_pages, scale, softcap, slopes, row_positions, out, lse, workspace,
+                                      workspace_bytes, stream);
+}
+
+static idx_status sparse_attention_call(AttentionLaunch* launch, const void* q, const void* latent_pages,
+                                        int32_t dtype, const int32_t* block_table, const int32_t* indices, int32_t k,
+                                        const int32_t* cu_q, int32_t rows, int32_t heads, int32_t requests,
+                                        int32_t next_n, int32_t num_pages, int32_t max_pages, float scale,
+                                        float softcap, const float* slopes, const int32_t* row_positions, void* out,
+                                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   const pmqa::LaunchEvents ev = take_events();
   pmqa::AttentionArgs a = attention_args(q, latent_pages, dtype, block_table, cu_q, rows, heads, requests, next_n,
                                          num_pages, max_pages, scale, softcap, slopes, row_positions, out, lse,
@@ -721,7 +773,28 @@ idx_status sparse_attention(const void* q, const void* latent_pages, int32_t dty
   const idx_status st = check_attention(a, indices, workspace_bytes,
                                         pmqa::attention_workspace_size(rows, heads, requests));
   if (st != IDX_OK) return st;
-  return from_hip(pmqa::launch_sparse_attention(a, static_cast<hipStream_t>(stream), ev));
+  return from_hip(launch(a, static_cast<hipStream_t>(stream), ev));
+}
+
+idx_status sparse_attention(const void* q, const void* latent_pages, int32_t dtype, const int32_t* block_table,
+                            const int32_t* indices, int32_t k, const int32_t* cu_q, int32_t rows, int32_t heads,
+                            int32_t requests, int32_t next_n, int32_t num_pages, int32_t max_pages, float scale,
+                            float softcap, const float* slopes, const int32_t* row_positions, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  return sparse_attention_call(pmqa::launch_sparse_attention, q, latent_pages, dtype, block_table, indices, k, cu_q,
+                               rows, heads, requests, next_n, num_pages, max_pages, scale, softcap, slopes,
+                               row_positions, out, lse, workspace, workspace_bytes, stream);
+}
+
+idx_status sparse_attention_mxfp4(const void* q, const uint8_t* latent_pages, int32_t dtype,
+                                  const int32_t* block_table, const int32_t* indices, int32_t k, const int32_t* cu_q,
+                                  int32_t rows, int32_t heads, int32_t requests, int32_t next_n, int32_t num_pages,
+                                  int32_t max_pages, float scale, float softcap, const float* slopes,
+                                  const int32_t* row_positions, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return sparse_attention_call(pmqa::launch_sparse_attention_mxfp4, q, latent_pages, dtype, block_table, indices, k,
+                               cu_q, rows, heads, requests, next_n, num_pages, max_pages, scale, softcap, slopes,
+                               row_positions, out, lse, workspace, workspace_bytes, stream);
 }
 
 idx_status hbm_gather_probe(const uint8_t* kv_pages, const float* k_scales, const int32_t* page_list,

@@ -626,5 +626,73 @@ int64_t pairs_together(const AttentionArgs& a) {
   return (static_cast<int64_t>(a.rows) + a.requests - 1) / a.requests * a.heads;
 }
 
+// Size of the pair tiles: the one whose estimated time is least, from what a
+// workgroup spends on each 64-key tile and on the call (16 / 32 / 64 / 128 pairs).
+// Tiles wider than the pairs would only idle.
+template <int KIND>
+int tile_pairs(const AttentionArgs& a, const double (&per_tile)[4], const double (&fixed)[4]) {
+  constexpr int kSizes[] = {16, 32, 64, 128};
+  const int64_t together = pairs_together<KIND>(a);
+  int best = 16;
+  double least = 1e300;
+  for (int i = 0; i < 4; ++i) {
+    const int m = kSizes[i];
+    if (i > 0 && together <= m / 2) break;
+    const int64_t pairs = static_cast<int64_t>(a.rows) * a.heads;
+    double tiles;
+    if (KIND == kSparse) {
+      tiles = static_cast<double>(a.rows) * ((a.heads + m - 1) / m) * ((a.k + kTile - 1) / kTile);
+    } else {
+      const double own = a.cu_q ? static_cast<double>(pairs / m + a.requests)
+                                : static_cast<double>(a.requests) * ((static_cast<int64_t>(a.next_n) * a.heads + m - 1) / m);
+      tiles = KIND == kShared ? static_cast<double>((pairs + m - 1) / m) * a.prefix_pages + own * (a.max_pages - a.prefix_pages)
+                              : own * a.max_pages;
+    }
+    const double t = tiles / kMaxGrid * per_tile[i] + fixed[i];
+    if (t < least) {
+      least = t;
+      best = m;
+    }
+  }
+  return best;
+}
+
+// One attention kernel over shares of the work list, and the join of what it split.
+template <int DT, int KIND, int M>
+hipError_t launch_joined(void (*kernel)(AttentionArgs, int, JoinInfo*, float*), int threads, const AttentionArgs& a,
+                         hipStream_t stream, LaunchEvents ev) {
+  const int64_t items = item_count<KIND, M>(a);
+  const int64_t tiles = KIND == kSparse ? (a.k + kTile - 1) / kTile : a.max_pages;
+  int grid = static_cast<int>(
+      std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + kItemCost<M>) / kMinUnits<M>)));
+  int min_units = kMinUnits<M>;
+  if (KIND == kSparse && !a.cu_q && items <= kMaxGrid / 2) {  // parts of one item each
+    grid = static_cast<int>(items * std::min<int64_t>(kMaxGrid / items, std::max<int64_t>(1, tiles / kMinTiles)));
+    min_units = 0;
+  }
+  JoinInfo* info = static_cast<JoinInfo*>(a.workspace);
+  float* pieces = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
+                                           join_bytes(KIND == kShared ? items : kMaxGrid));
+  const bool joins = KIND == kShared || grid > 1;
+  launch_kernel(kernel, dim3(grid), dim3(threads), stream, ev.start, joins ? nullptr : ev.stop, a, min_units, info,
+                pieces);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !joins) return e;
+  const JoinArgs j{info, pieces, a.out, a.lse};
+  if constexpr (KIND == kShared) {
+    const int64_t pairs = static_cast<int64_t>(a.rows) * a.heads;
+    launch_kernel(join_shared_kernel<DT>, dim3(static_cast<uint32_t>((pairs + 3) / 4)), dim3(256), stream, nullptr,
+                  ev.stop, j, M, pairs, a.heads, a.next_n);
+  } else {
+    // (at 16 pairs, 14 -> 7 us where requests of up to 32768 keys have up to 35
+    // pieces; at 32 pairs and 8 pieces 6 -> 7 us)
+    if (M == 16)
+      launch_kernel(join_kernel<DT, true>, dim3(M, grid), dim3(256), stream, nullptr, ev.stop, j, M);
+    else
+      launch_kernel(join_kernel<DT, false>, dim3(M / 4, grid), dim3(256), stream, nullptr, ev.stop, j, M);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 }  // namespace pmqa

@@ -70,5 +70,8 @@ size_t shared_prefix_workspace_size(int32_t rows, int32_t heads, int32_t request
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
 hipError_t launch_shared_prefix_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
 hipError_t launch_sparse_attention(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_paged_attention_mxfp4(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_shared_prefix_attention_mxfp4(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
+hipError_t launch_sparse_attention_mxfp4(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev = {});
 
 }  // namespace pmqa
