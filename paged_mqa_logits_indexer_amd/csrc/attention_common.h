@@ -125,6 +125,9 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 
 typedef __attribute__((address_space(3))) const s16x8* LdsVec8;
 typedef __attribute__((address_space(3))) s16x4* LdsVec4;
+__device__ __forceinline__ void lds_write(uint32_t at, s16x8 x) {
+  *reinterpret_cast<__attribute__((address_space(3))) s16x8*>(at) = x;
+}
 __device__ __forceinline__ s16x8 lds_read(uint32_t at) { return *reinterpret_cast<LdsVec8>(at); }
 __device__ __forceinline__ s16x4 lds_read_tr(uint32_t at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<LdsVec4>(at));
