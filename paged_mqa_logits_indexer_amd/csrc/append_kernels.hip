@@ -146,35 +146,58 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(
   *reinterpret_cast<i32x4*>(out) = pack16<DT>(x);
 }
 
-// Four threads per block of 32 dimensions, 8 each, and 8 for the rotated part: 72
-// of a row, as above.
+// e2m1_codes by the conversion instruction, two values at a time (nearest even, to
+// +-6 at most; it takes the power of two from its operand's exponent): with the
+// comparisons of e2m1_code, which 32 values of a thread's own make its whole time,
+// 8191 rows 10.8 us instead of 6.0.
+__device__ __forceinline__ uint32_t packed_e2m1(const F32Row& x, int code) {
+  const float power = __uint_as_float(static_cast<uint32_t>(code) << 23);
+  uint32_t y = 0;
+  y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x.v[0], x.v[1], power, 0);
+  y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x.v[2], x.v[3], power, 1);
+  y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x.v[4], x.v[5], power, 2);
+  y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x.v[6], x.v[7], power, 3);
+  return code < 255 ? y : 0u;
+}
+
+// 32 threads per token: 16 take a block of 32 dimensions each, its largest magnitude
+// and codes in their own registers, 8 an eighth of the rotated part.
+constexpr int kPackThreads = 32;
 template <int DT>
 __global__ __launch_bounds__(kThreads) void latent_append_mxfp4_kernel(
     const char* __restrict__ kv, int64_t kv_stride, const int32_t* __restrict__ positions,
     const int32_t* __restrict__ slots, const float* __restrict__ rope, int max_positions, int interleaved,
     int tokens, int total_slots, char* __restrict__ pages) {
-  const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
-  const int token = at / kRowPieces, piece = at % kRowPieces;
-  if (token >= tokens) return;  // (72 and 256 are multiples of 4: the threads of a block leave together)
-  const int slot = slots[token];
-  if (slot < 0 || slot >= total_slots) return;
+  const int token = blockIdx.x * (kThreads / kPackThreads) + static_cast<int>(threadIdx.x) / kPackThreads;
+  const int part = threadIdx.x % kPackThreads;
+  if (token >= tokens) return;
   const char* row = kv + static_cast<int64_t>(token) * kv_stride * 2;
+  const int slot = slots[token];
+  const bool here = slot >= 0 && slot < total_slots;
   char* out = pages + static_cast<int64_t>(slot) * IDX_LATENT_MXFP4_ROW;
-  F32Row x = load8<DT>(row + piece * 16);
-  if (piece < kLatentPieces) {
-    uint32_t amax = amax_bits(x);
-    amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 1)));
-    amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 2)));
+  if (part < IDX_LATENT_DIM / 32) {
+    F32Row x[4];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = load8<DT>(row + part * 64 + i * 16);
+      amax = max(amax, amax_bits(x[i]));
+    }
     const int code = block_power(amax);
-    reinterpret_cast<uint32_t*>(out)[piece] = e2m1_codes(x, code);
-    if ((piece & 3) == 0) out[IDX_LATENT_DIM / 2 + piece / 4] = static_cast<char>(code);
-    return;
+    i32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = static_cast<int>(packed_e2m1(x[i], code));
+    if (!here) return;
+    reinterpret_cast<i32x4*>(out)[part] = y;
+    out[IDX_LATENT_DIM / 2 + part] = static_cast<char>(code);
+  } else if (part < IDX_LATENT_DIM / 32 + kRope / 8) {
+    const int piece = part - IDX_LATENT_DIM / 32;
+    const int pos = max(0, min(positions[token], max_positions - 1));
+    F32Row x = load8<DT>(row + kLatentPieces * 16 + piece * 16);
+    const F32Row other = load8<DT>(row + kLatentPieces * 16 + (piece ^ 4) * 16);
+    rotate8<DT>(x, other, piece, interleaved != 0, rope + static_cast<int64_t>(pos) * kRope);
+    if (here) reinterpret_cast<i32x4*>(out + kPacked)[piece] = pack16<DT>(x);
   }
-  const int pos = max(0, min(positions[token], max_positions - 1));
-  const int rotated = piece - kLatentPieces;
-  const F32Row other = load8<DT>(row + (piece ^ 4) * 16);
-  rotate8<DT>(x, other, rotated, interleaved != 0, rope + static_cast<int64_t>(pos) * kRope);
-  reinterpret_cast<i32x4*>(out + kPacked)[rotated] = pack16<DT>(x);
 }
 
 template <int DT>
@@ -194,7 +217,7 @@ void launch_index(const AppendArgs& a, hipStream_t stream, LaunchEvents ev) {
 
 template <int DT>
 void launch_latent(const AppendArgs& a, bool mxfp4, hipStream_t stream, LaunchEvents ev) {
-  const int64_t pieces = static_cast<int64_t>(a.tokens) * kRowPieces;
+  const int64_t pieces = static_cast<int64_t>(a.tokens) * (mxfp4 ? kPackThreads : kRowPieces);
   launch_kernel(mxfp4 ? latent_append_mxfp4_kernel<DT> : latent_append_kernel<DT>,
                 dim3(static_cast<uint32_t>((pieces + kThreads - 1) / kThreads)),
                 dim3(kThreads), stream, ev.start, ev.stop, static_cast<const char*>(a.rows), a.row_stride, a.positions,

@@ -202,14 +202,20 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
         for (int i = 0; i < 4; ++i) {
           const s16x8 x = dequant8<DT>(static_cast<uint32_t>(codes[j][i]), power);
           s[i & 1] = E::mfma32(x, *reinterpret_cast<const s16x8*>(s_query + (4 * j + i) * 1024), s[i & 1]);
-          // (a row that sees a NaN has it from the score; others must not meet it)
-          *reinterpret_cast<s16x8*>(image + (k_at ^ (i * 16)) + j * 2048) = mixed ? finite_or_zero<DT>(x) : x;
+          *reinterpret_cast<s16x8*>(image + (k_at ^ (i * 16)) + j * 2048) = x;
         }
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         s[j] = E::mfma32(__builtin_bit_cast(s16x8, rotated[j]),
                          *reinterpret_cast<const s16x8*>(s_query + (16 + j) * 1024), s[j]);
+      if (mixed) {  // (a row that sees a NaN has it from the score; others must not meet it)
+#pragma unroll 1
+        for (int i = 0; i < kOwnImage / 1024; ++i) {
+          s16x8* v = reinterpret_cast<s16x8*>(image + i * 1024) + lane;
+          *v = finite_or_zero<DT>(*v);
+        }
+      }
       const uint32_t live = live_next;  // sparse: bits of the block's keys
       if (block + kWaves < block_end) load_block(block + kWaves);
       float z[4];

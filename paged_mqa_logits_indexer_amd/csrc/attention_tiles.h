@@ -135,7 +135,34 @@ struct Packed {
   i32x4 codes[2], rotated;
   uint32_t power[2];
 };
+__device__ __forceinline__ uint32_t lds_read_byte(uint32_t at) {
+  return *reinterpret_cast<__attribute__((address_space(3))) const uint8_t*>(at);
+}
+template <int LEFT>
+__device__ __forceinline__ void wait_loads() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | ((LEFT >> 4) << 14));  // vmcnt(LEFT) alone
+  __asm__ volatile("" ::: "memory");
+}
 constexpr int kPackedParts = 5;  // loads of it
+// MX, wide: the keys come by direct loads, three steps ahead, and wait in LDS until
+// they are unpacked; the image then needs three slots instead of four.  A wave's 8
+// keys are four pieces of 128 bytes of each: two of codes, one that begins with the
+// powers, and the rotated part (bytes 272 .. 383 are loaded twice: four whole
+// instructions instead of three and an eighth of one).
+constexpr int kStageAt = 3 * 32 * kRowBytes, kStageBytes = 4 * 1024, kStageLoads = 4;
+static_assert(kStageAt + 4 * 2 * kStageBytes <= kRingBytes, "two steps of packed keys behind the image");
+template <int J>
+__device__ __forceinline__ void load_stage(const char* at, uint32_t lds) {
+  constexpr int kFrom = J < 3 ? J * 128 : kRotatedAt;
+  __asm__ volatile(
+      "s_add_u32 m0, %0, %2\n"
+      "s_nop 0\n"
+      "global_load_lds_dwordx4 %1, off offset:%3"
+      :
+      : "s"(lds), "v"(at), "n"(J * 1024 - kFrom), "n"(kFrom)
+      : "memory", "m0", "scc");
+}
 __device__ __forceinline__ void load_packed(Packed& x, const char* row, int part) {
   const int c8 = lane_id() & 7;
   switch (part) {
@@ -154,6 +181,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   using S = Shape<M>;
   constexpr int kStepsPerTile = kTile / S::kKeys;
   constexpr int ST = S::kBlocks;
+  constexpr bool kStaged = MX && S::kWide;
+  constexpr int kAhead = kStaged ? 3 : S::kDistance;  // steps that are loaded ahead
   __shared__ __attribute__((aligned(1024))) char s_keys[kRingBytes];
   __shared__ int s_rows[KIND == kSparse ? kWindow : 1];       // sparse: cache row of each listed key, -1: none
   __shared__ uint32_t s_live[S::kSlots][4];                   // sparse: bits of the keys that are there
@@ -251,8 +280,11 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     // MX: the keys between memory and LDS, and which of them are there
     Packed packed[MX ? S::kOctets : 1];
     uint32_t packed_live = 0;
-    // (the wide form also loads the two steps after the last, from the row of
-    // zeros: it then has no branch between its MFMAs)
+    // (the wide form also loads the steps after the last, from the row of zeros: it
+    // then has no branch between its MFMAs)
+    auto slot_base = [&](int step) {
+      return kStaged ? (step - step0) % 3 * S::kSlotBytes : ((step - step0) & (S::kSlots - 1)) * S::kSlotBytes;
+    };
     auto locate = [&](int step) {
       const int slot = (step - step0) & (S::kSlots - 1);
       const bool any = step < step_end;
@@ -292,6 +324,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
           live = any && tok >= it.min_start && tok < it.max_end;
         }
         from[o] = live ? cache + static_cast<int64_t>(row) * (MX ? IDX_LATENT_MXFP4_ROW : kRowBytes) : zero;
+        if constexpr (kStaged) from[o] += (lane & 7) * 16;
         if constexpr (!MX) {
           from[o] += ((lane & 7) ^ swz((8 * ((wave * S::kOctets + o) & 1)) + (lane >> 3))) * 16;
           to[o] = ring + slot * S::kSlotBytes + (wave * S::kOctets + o) * kOctBytes;
@@ -303,7 +336,25 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     // MX: one of the nine 16-byte pieces of this lane's part of an octet into the image,
     // whose place for the step's codes is pack_base(step).  (The second octet's keys
     // exchange their chunks by bit 1 more than the first's.)
-    auto pack_base = [&](int step) { return opaque(ring + ((step - step0) & (S::kSlots - 1)) * S::kSlotBytes + pack_at); };
+    auto pack_base = [&](int step) { return opaque(ring + slot_base(step) + pack_at); };
+    auto stage_of = [&](int step) { return ring + kStageAt + (wave * 2 + ((step - step0) & 1)) * kStageBytes; };
+    auto load_staged = [&](int step, int j) {  // j is a constant of the unrolled loop
+      const uint32_t to = stage_of(step);
+      switch (j) {
+        case 0: return load_stage<0>(from[0], to);
+        case 1: return load_stage<1>(from[0], to);
+        case 2: return load_stage<2>(from[0], to);
+        case 3: return load_stage<3>(from[0], to);
+      }
+    };
+    // (a key's 16 powers are at 128 times its number in the third piece)
+    auto read_staged = [&](uint32_t stage, int part) {
+      const uint32_t at = stage + lane * 16, power = stage + 2048 + (lane >> 3) * 128 + (lane & 7);
+      if (part == 0) packed[0].codes[0] = __builtin_bit_cast(i32x4, lds_read(at)), packed[0].power[0] = lds_read_byte(power);
+      if (part == 1)
+        packed[0].codes[1] = __builtin_bit_cast(i32x4, lds_read(at + 1024)), packed[0].power[1] = lds_read_byte(power + 8);
+      if (part == 2) packed[0].rotated = __builtin_bit_cast(i32x4, lds_read(at + 3072));
+    };
     auto unpack = [&](uint32_t base, int step, int o, int j) {
       if (j < 8) {
         const float power = __uint_as_float(packed[o].power[j >> 2] << 23);
@@ -327,6 +378,11 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     };
     auto fetch_all = [&](int step) {
       locate(step);
+      if constexpr (kStaged) {
+#pragma unroll
+        for (int j = 0; j < kStageLoads; ++j) load_staged(step, j);
+        return;
+      }
 #pragma unroll
       for (int o = 0; o < S::kOctets; ++o)
 #pragma unroll
@@ -390,7 +446,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       load_octet(from, q_ring + o * kOctBytes);
     }
     // narrow: slot 0 holds step0's keys, slot 1 the queries
-    if constexpr (MX) fetch_all(step0);
+    if constexpr (MX && !kStaged) fetch_all(step0);
     else if constexpr (!S::kWide) issue(step0);
     wait_and_barrier<0>();
     s16x8 q[kQ];
@@ -408,9 +464,17 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         q[ks] = lds_read(q_ring + pg * 16 * kRowBytes + (k_at ^ ((ks & 1) * 64)) + (ks >> 1) * 1024);
     }
     lds_barrier();
-    if constexpr (MX) {
+    if constexpr (kStaged) {
+      fetch_all(step0);
+      fetch_all(step0 + 1);
+      wait_loads<kStageLoads>();
+#pragma unroll
+      for (int j = 0; j < 3; ++j) read_staged(stage_of(step0), j);
       unpack_all(step0);
-      if (S::kWide || step0 + 1 < step_end) fetch_all(step0 + 1);
+      fetch_all(step0 + 2);
+    } else if constexpr (MX) {
+      unpack_all(step0);
+      if (step0 + 1 < step_end) fetch_all(step0 + 1);
     } else if constexpr (S::kWide) {
 #pragma unroll
       for (int d = 0; d < S::kDistance; ++d) issue(step0 + d);
@@ -493,12 +557,12 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     auto do_step = [&](int step) -> bool {
       // the step's keys are in their slot, and every wave has left the slot
       // that the next issue fills
-      if constexpr (MX) {
+      if constexpr (kStaged) {
+        wait_and_barrier<kStageLoads>();  // all but the loads of the step after next
+      } else if constexpr (MX) {
         lds_barrier();
-        if constexpr (!S::kWide) {
-          if (step + 1 < step_end) unpack_all(step + 1);
-          if (step + 2 < step_end) fetch_all(step + 2);
-        }
+        if (step + 1 < step_end) unpack_all(step + 1);
+        if (step + 2 < step_end) fetch_all(step + 2);
       } else if constexpr (S::kWide) {
         wait_and_barrier<S::kOctets * kOctLoads>();  // all but the next step's
       } else {
@@ -506,7 +570,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         if (step + S::kDistance < step_end) issue(step + S::kDistance);
       }
       const int slot = (step - step0) & (S::kSlots - 1);
-      const uint32_t base = ring + slot * S::kSlotBytes + (S::kWide ? 0 : ts * ST * kBlkBytes);
+      const uint32_t base = ring + slot_base(step) + (S::kWide ? 0 : ts * ST * kBlkBytes);
 
       // ---- S = K Q^T
       float z[kScores];
@@ -524,8 +588,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ks = 0; ks < kRing - 2; ++ks) read(ks);
+        if constexpr (kStaged) read_staged(stage_of(step + 1), 0);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!MX || KIND == kSparse) locate(step + S::kDistance);  // while they come
+        if constexpr (!MX || KIND == kSparse) locate(step + kAhead);  // while they come
         const uint32_t image = MX ? pack_base(step + 1) : 0;
 #pragma unroll
         for (int ks = 0; ks < kQ; ks += 2) {
@@ -536,12 +601,16 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
           s0 = E::mfma_wide(kk[ks % kRing], q[ks], s0);
           s0 = E::mfma_wide(kk[(ks + 1) % kRing], q[ks + 1], s0);
           if (ks / 2 < kOctLoads) {
-            if constexpr (MX) unpack(image, step + 1, 0, ks / 2);
-            else load_one(ks / 2);
-            if (MX && KIND != kSparse && ks / 2 == kOctLoads - 1) locate(step + S::kDistance);
+            if constexpr (MX) {
+              unpack(image, step + 1, 0, ks / 2);
+              if (ks / 2 == 1 || ks / 2 == 5) read_staged(stage_of(step + 1), ks / 2 == 1 ? 1 : 2);
+              if (KIND != kSparse && ks / 2 == kOctLoads - 1) locate(step + kAhead);
+            } else {
+              load_one(ks / 2);
+            }
           } else if (ks / 2 - kOctLoads < 8) {
             weigh(ks / 2 - kOctLoads, sum);
-            if (MX && ks / 2 - kOctLoads < kPackedParts) load_packed(packed[0], from[0], ks / 2 - kOctLoads);
+            if (kStaged && ks / 2 - kOctLoads < kStageLoads) load_staged(step + kAhead, ks / 2 - kOctLoads);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -643,7 +712,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       auto clear_nonfinite = [&] {
         __syncthreads();
         for (int i = tid; i < S::kSlotBytes / 16; i += kAttnThreads) {
-          s16x8* v = reinterpret_cast<s16x8*>(s_keys + slot * S::kSlotBytes) + i;
+          s16x8* v = reinterpret_cast<s16x8*>(s_keys + slot_base(step)) + i;
           s16x8 x = *v;
           constexpr int kExp = DT == IDX_BF16 ? 0x7F80 : 0x7C00;
 #pragma unroll
@@ -662,7 +731,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         // before it: weights of zero on its own keys, which every row of the
         // pair tile sees or whose non-finite values have been cleared.)
         float mx = -__builtin_inff(), kept = 0.0f;
-        value_wide(step > step0 ? ring + ((step - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes : base, [&](int d) {
+        value_wide(step > step0 ? ring + slot_base(step - 1) : base, [&](int d) {
           if (d < 8) {
             z[2 * d] *= z_scale;
             z[2 * d + 1] *= z_scale;
@@ -769,7 +838,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       for (int d = 0; d < kAccs; ++d) pin(acc[d]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) weigh(i, l);
-      value_wide(ring + ((step_end - step0 - 1) & (S::kSlots - 1)) * S::kSlotBytes, [&](int d) {
+      value_wide(ring + slot_base(step_end - 1), [&](int d) {
         if (d < 8) keep(d, l_kept);
       });
     } else {
