@@ -115,6 +115,12 @@ __device__ __attribute__((aligned(128))) const uint32_t kZeroRow[IDX_LATENT_ROW 
 // spreads the K operand's 128-bit reads and V's transposing 64-bit reads over all
 // banks (attention_kernels.hip).
 __device__ __forceinline__ int swz(int key) { return (((key >> 1) & 1) << 2) | (-(key >> 2) & 3); }
+// Keys that are written to LDS from registers (MX) also exchange by their last bit:
+// eight lanes that write the same chunk of eight keys then take all 32 banks of a
+// write, where pairs of keys took the same ones.  The reads' 64 banks hold even and
+// odd keys apart, so nothing changes for them.
+template <bool MX>
+__device__ __forceinline__ int swz_of(int key) { return MX ? swz(key) ^ (key & 1) : swz(key); }
 
 // A value whose origin the compiler does not see: constants added to such an
 // LDS address become the read's own offset instead of an addition per read.

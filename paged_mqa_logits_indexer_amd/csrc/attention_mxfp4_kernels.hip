@@ -73,9 +73,9 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
   const char* s_query = s_ring + kQueryAt + lane * 16;
   auto place = [](int key) { return (key >> 3) * kOwnOctet + (key & 7) * 128; };
   const int vkey = 4 * g4 + (n16 >> 2);
-  const uint32_t k_at = place(n16) + (g4 >> 1) * 1024 + (((g4 & 1) * 4) ^ swz(n16)) * 16;
+  const uint32_t k_at = place(n16) + (g4 >> 1) * 1024 + (((g4 & 1) * 4) ^ swz_of<true>(n16)) * 16;
   const uint32_t v_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)image)) +
-                        place(vkey) + (((n16 >> 1) & 1) ^ swz(vkey)) * 16 + (n16 & 1) * 8;
+                        place(vkey) + (((n16 >> 1) & 1) ^ swz_of<true>(vkey)) * 16 + (n16 & 1) * 8;
 
   const int items = static_cast<int>(item_count<KIND, M>(a));
   int64_t at = share.t0;

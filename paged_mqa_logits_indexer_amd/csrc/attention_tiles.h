@@ -127,7 +127,7 @@ __device__ __forceinline__ s16x8 dequant8(uint32_t codes, float power) {
   return __builtin_bit_cast(s16x8, x);
 }
 
-// MX: what a lane holds of a 4-bit key (lane / 8 of an octet) between memory and
+// MX: what a lane holds of a 4-bit key (lane % 8 of an octet) between memory and
 // LDS: two blocks of 32 codes, their powers of two, and 8 of the rotated part.
 constexpr int kPowersAt = kValDim / 2;               // 16 power bytes behind the codes
 constexpr int kRotatedAt = kPowersAt + kValDim / 32;
@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_stage(const char* at, uint32_t lds) {
       : "memory", "m0", "scc");
 }
 __device__ __forceinline__ void load_packed(Packed& x, const char* row, int part) {
-  const int c8 = lane_id() & 7;
+  const int c8 = lane_id() >> 3;
   switch (part) {
     case 0: x.codes[0] = *reinterpret_cast<const i32x4*>(row + c8 * 16); break;
     case 1: x.power[0] = static_cast<uint8_t>(row[kPowersAt + c8]); break;
@@ -209,18 +209,18 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   uint32_t k_at, v_at;
   if constexpr (S::kWide) {
     const int key = lane & 31, vkey = 4 * half + (n16 >> 2);
-    k_at = key_offset(key) + (half ^ swz(key)) * 16;
-    v_at = key_offset(vkey) + (((2 * (g4 & 1) + ((lane & 3) >> 1)) ^ swz(vkey)) * 16) + (lane & 1) * 8;
+    k_at = key_offset(key) + (half ^ swz_of<MX>(key)) * 16;
+    v_at = key_offset(vkey) + (((2 * (g4 & 1) + ((lane & 3) >> 1)) ^ swz_of<MX>(vkey)) * 16) + (lane & 1) * 8;
   } else {
     const int vkey = 4 * g4 + (n16 >> 2);
-    k_at = key_offset(n16) + (g4 ^ swz(n16)) * 16;
-    v_at = key_offset(vkey) + (((n16 >> 1) & 1) ^ swz(vkey)) * 16 + (n16 & 1) * 8;
+    k_at = key_offset(n16) + (g4 ^ swz_of<MX>(n16)) * 16;
+    v_at = key_offset(vkey) + (((n16 >> 1) & 1) ^ swz_of<MX>(vkey)) * 16 + (n16 & 1) * 8;
   }
   // MX: where this lane's first chunk of codes goes in a slot
   uint32_t pack_at = 0;
   if constexpr (MX) {
-    const int key = wave * (8 * S::kOctets) + (lane >> 3);
-    pack_at = key_offset(key) + ((lane & 7) >> 1) * 1024 + (((lane & 1) * 4) ^ swz(key & 15)) * 16;
+    const int key = wave * (8 * S::kOctets) + (lane & 7), c = lane >> 3;
+    pack_at = key_offset(key) + (c >> 1) * 1024 + (((c & 1) * 4) ^ swz_of<MX>(key & 15)) * 16;
   }
   const int capacity = a.max_pages * kPage;
   const char* cache = static_cast<const char*>(a.cache);
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       uint32_t live_bits = 0;
 #pragma unroll
       for (int o = 0; o < S::kOctets; ++o) {
-        const int key = key0 + 8 * o + (lane >> 3);
+        const int key = key0 + 8 * o + (MX && !kStaged ? lane & 7 : lane >> 3);
         int row;
         bool live;
         if constexpr (KIND == kSparse) {
@@ -316,7 +316,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
           live = any && row >= 0;
           const uint64_t mask = __ballot(live);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) live_bits |= static_cast<uint32_t>(mask >> (8 * i) & 1) << (8 * o + i);
+          for (int i = 0; i < 8; ++i)
+            live_bits |= static_cast<uint32_t>(mask >> (MX && !kStaged ? i : 8 * i) & 1) << (8 * o + i);
         } else {
           // keys that no row of the pair tile sees are not read
           const int tok = it.tile0 * kTile + key;
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
           live = any && tok >= it.min_start && tok < it.max_end;
         }
         from[o] = live ? cache + static_cast<int64_t>(row) * (MX ? IDX_LATENT_MXFP4_ROW : kRowBytes) : zero;
-        if constexpr (kStaged) from[o] += (lane & 7) * 16;
+        if constexpr (kStaged) from[o] += ((lane & 7) ^ (lane >> 3)) * 16;
         if constexpr (!MX) {
           from[o] += ((lane & 7) ^ swz((8 * ((wave * S::kOctets + o) & 1)) + (lane >> 3))) * 16;
           to[o] = ring + slot * S::kSlotBytes + (wave * S::kOctets + o) * kOctBytes;
@@ -347,9 +348,11 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
         case 3: return load_stage<3>(from[0], to);
       }
     };
-    // (a key's 16 powers are at 128 times its number in the third piece)
+    // (a key's 16-byte chunks are exchanged by its number, the first one of the third
+    // piece holds its powers)
     auto read_staged = [&](uint32_t stage, int part) {
-      const uint32_t at = stage + lane * 16, power = stage + 2048 + (lane >> 3) * 128 + (lane & 7);
+      const uint32_t key = stage + (lane & 7) * 128, c = lane >> 3;
+      const uint32_t at = key + (c ^ (lane & 7)) * 16, power = key + 2048 + (lane & 7) * 16 + c;
       if (part == 0) packed[0].codes[0] = __builtin_bit_cast(i32x4, lds_read(at)), packed[0].power[0] = lds_read_byte(power);
       if (part == 1)
         packed[0].codes[1] = __builtin_bit_cast(i32x4, lds_read(at + 1024)), packed[0].power[1] = lds_read_byte(power + 8);
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
                   dequant8<DT>(static_cast<uint32_t>(packed[o].codes[j >> 2][j & 3]), power));
       } else {
         // from chunk 4 (c8 & 1) of piece c8 / 2 to chunk c8 of piece 8
-        const uint32_t c = opaque(tid) & 7;
+        const uint32_t c = (opaque(tid) & 63) >> 3;
         lds_write((base ^ ((c ^ (c & 1) * 4 ^ 2 * o) * 16)) + o * kOctBytes + (8 - (c >> 1)) * 1024,
                   __builtin_bit_cast(s16x8, packed[o].rotated));
         if (KIND == kSparse && !S::kWide && o == S::kOctets - 1 && lane == 0)
@@ -442,7 +445,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
     for (int o = wave; o < M / 8; o += 4) {
       const int pair = 8 * o + (lane >> 3);
       const char* from = (pair < it.pairs ? static_cast<const char*>(a.q) + (pair_base + pair) * kRowBytes : zero) +
-                         (((lane & 7) ^ swz(pair & 15)) * 16);
+                         (((lane & 7) ^ swz_of<MX>(pair & 15)) * 16);
       load_octet(from, q_ring + o * kOctBytes);
     }
     // narrow: slot 0 holds step0's keys, slot 1 the queries
