@@ -26,13 +26,16 @@ def release(table, lens, ended, refs):
 
 
 def fork(table, lens, parents, refs):
-    """-> (table, lens, refs, src, dst, tokens, [taken, without])."""
+    """-> (table, lens, refs, src, dst, tokens, [taken, without]).  Pages are taken
+    before the shared ones are counted (which matters only where refs and table
+    contradict each other: a page of the table without a holder)."""
     table, refs, after = [list(row) for row in table], list(refs), list(lens)
     n = len(lens)
     free = [p for p, r in enumerate(refs) if r <= 0]
     src, dst, tokens, without = [-1] * n, [-1] * n, [0] * n, 0
     taken = 0
     before = [list(row) for row in table]
+    shared = []
     for b, p in enumerate(parents):
         if not 0 <= p < n or lens[b] > 0:
             continue
@@ -42,15 +45,17 @@ def fork(table, lens, parents, refs):
             without += 1
             continue
         for j in range(full):
-            page = table[b][j] = before[p][j]
-            if 0 <= page < len(refs):
-                refs[page] += 1
+            shared.append(before[p][j])
+            table[b][j] = before[p][j]
         if rest:
             src[b], dst[b], tokens[b] = before[p][full], free[taken], rest
             taken += 1
             table[b][full] = dst[b]
             refs[dst[b]] = 1
         after[b] = length
+    for page in shared:
+        if 0 <= page < len(refs):
+            refs[page] += 1
     return table, after, refs, src, dst, tokens, [taken, without]
 
 

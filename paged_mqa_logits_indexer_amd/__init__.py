@@ -771,11 +771,11 @@ def axis_rotations(positions, axis_map, rope, out, events=None):
 def _strided_rows(t, name, dtype, dev, shape):
     """Strides of [tokens, heads, dim] rows; those of a dimension of one element
     carry no meaning and become those of a packed tensor."""
-    _need(t, name, dtype, dev, 3)
-    if t.shape != shape or t.stride(2) != 1:
+    token, head, unit = t.stride() if isinstance(t, torch.Tensor) and t.dim() == 3 else (0, 0, 0)
+    if not (unit == 1 and t.shape == shape and t.dtype is dtype and t.is_cuda and t.device == dev):
+        _need(t, name, dtype, dev, 3)
         raise ValueError(f"{name} must be {list(shape)} with unit stride in the last dimension")
     tokens, heads, dim = shape
-    token, head = t.stride(0), t.stride(1)
     if heads == 1:
         head = dim
     if tokens == 1:
@@ -873,9 +873,9 @@ def pages_workspace_bytes(requests: int, num_pages: int) -> int:
     return int(load_library().pages_workspace_bytes(int(requests), int(num_pages)))
 
 
-def _pool(block_table, lens, refs, **others):
-    """Shapes of a pool: requests, max_pages, num_pages; ``others`` (tensor, "requests"
-    or "pages" or a number of elements)."""
+def _pool(block_table, lens, refs, of_requests, of_pages):
+    """Shapes of a pool -- requests, max_pages, num_pages -- and the checks of the
+    tensors, by name, that hold an int32 for each request and for each page."""
     dev = block_table.device
     if block_table.dim() != 2:
         raise ValueError(f"block_table must have 2 dims, got {tuple(block_table.shape)}")
@@ -884,9 +884,10 @@ def _pool(block_table, lens, refs, **others):
     _need_shaped(block_table, "block_table", torch.int32, dev, (requests, max_pages))
     _need_shaped(lens, "lens", torch.int32, dev, (requests,))
     _need_shaped(refs, "refs", torch.int32, dev, (num_pages,))
-    for name, (t, size) in others.items():
-        size = requests if size == "requests" else num_pages if size == "pages" else size
-        _need_shaped(t, name, torch.int32, dev, (size,))
+    for name, t in of_requests.items():
+        _need_shaped(t, name, torch.int32, dev, (requests,))
+    for name, t in of_pages.items():
+        _need_shaped(t, name, torch.int32, dev, (num_pages,))
     return dev, requests, max_pages, num_pages
 
 
@@ -907,8 +908,8 @@ def release_pages(block_table, lens, ended, refs, new_lens, new_refs, events=Non
     free); ended [requests] int32.  new_lens and new_refs are written, and may be
     lens and refs.
     """
-    dev, requests, max_pages, num_pages = _pool(block_table, lens, refs, ended=(ended, "requests"),
-                                                new_lens=(new_lens, "requests"), new_refs=(new_refs, "pages"))
+    dev, requests, max_pages, num_pages = _pool(block_table, lens, refs, dict(ended=ended, new_lens=new_lens),
+                                                dict(new_refs=new_refs))
     _launch("release_pages", dev, events, block_table.data_ptr(), lens.data_ptr(), ended.data_ptr(), requests,
             max_pages, refs.data_ptr(), num_pages, new_lens.data_ptr(), new_refs.data_ptr())
 
@@ -926,9 +927,9 @@ def fork_pages(block_table, lens, parents, refs, new_lens, new_refs, src, dst, t
     the call when None.
     """
     dev, requests, max_pages, num_pages = _pool(
-        block_table, lens, refs, parents=(parents, "requests"), new_lens=(new_lens, "requests"),
-        new_refs=(new_refs, "pages"), src=(src, "requests"), dst=(dst, "requests"), tokens=(tokens, "requests"),
-        counts=(counts, 2))
+        block_table, lens, refs, dict(parents=parents, new_lens=new_lens, src=src, dst=dst, tokens=tokens),
+        dict(new_refs=new_refs))
+    _need_shaped(counts, "counts", torch.int32, dev, (2,))
     workspace = _pool_workspace(workspace, requests, num_pages, dev)
     _launch("fork_pages", dev, events, block_table.data_ptr(), lens.data_ptr(), parents.data_ptr(), requests,
             max_pages, refs.data_ptr(), num_pages, new_lens.data_ptr(), new_refs.data_ptr(), src.data_ptr(),
@@ -944,8 +945,8 @@ def compact_pages(block_table, lens, refs, new_table, new_refs, src, dst, counts
     new_table [requests, max_pages] and new_refs [num_pages] say where the pages
     then are, and may be block_table and refs.
     """
-    dev, requests, max_pages, num_pages = _pool(block_table, lens, refs, new_refs=(new_refs, "pages"),
-                                                src=(src, "pages"), dst=(dst, "pages"), counts=(counts, 2))
+    dev, requests, max_pages, num_pages = _pool(block_table, lens, refs, {}, dict(new_refs=new_refs, src=src, dst=dst))
+    _need_shaped(counts, "counts", torch.int32, dev, (2,))
     _need_shaped(new_table, "new_table", torch.int32, dev, (requests, max_pages))
     workspace = _pool_workspace(workspace, requests, num_pages, dev)
     _launch("compact_pages", dev, events, block_table.data_ptr(), lens.data_ptr(), requests, max_pages,

@@ -357,8 +357,16 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
   }
 }
 
-// Microseconds of a workgroup per 64-key tile, and of a call.
-constexpr double kPerTile[] = {1.5, 2.1, 3.5, 4.2}, kFixed[] = {15, 20, 32, 65};
+// Microseconds of a workgroup per 64-key tile, and of a call, over pages and over
+// selections (whose keys each pair tile gathers for itself), from every size forced on
+// selections of 512 and 2048 keys for 1 .. 256 rows of 32, 64 and 128 heads, and on 1
+// .. 64 requests of 512 .. 32768 keys with 16 .. 128 heads.  Between them (16 / 32 / 64
+// / 128 pairs): 64 rows of 32 heads over 2048 keys 47 / 45 / 54 / 73 us, 256 rows of 64
+// heads 190 / 173 / 129 / 190, of 128 heads 369 / 336 / 250 / 213; 16 requests of 32768
+// keys with 32 heads 86 / 98 / 128 / 173, with 64 heads 148 / 161 / 132 / 179, with 128
+// heads 267 / 297 / 225 / 200.
+constexpr double kPerTile[2][4] = {{0.95, 2.1, 3.1, 4.8}, {1.35, 2.4, 3.45, 5.0}};
+constexpr double kFixed[2][4] = {{19, 22, 27, 47}, {17, 18, 24, 45}};
 
 template <int DT, int KIND, int M>
 hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
@@ -368,7 +376,7 @@ hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
 
 template <int DT, int KIND>
 hipError_t launch_kind(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
-  switch (tile_pairs<KIND>(a, kPerTile, kFixed)) {
+  switch (tile_pairs<KIND>(a, kPerTile[KIND == kSparse], kFixed[KIND == kSparse])) {
     case 16: return launch<DT, KIND, 16>(a, stream, ev);
     case 32: return launch<DT, KIND, 32>(a, stream, ev);
     case 64: return launch<DT, KIND, 64>(a, stream, ev);

@@ -116,6 +116,38 @@ def test_fork_of_one_parent_many_times(gpu):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("free", ["none", "last", "some", "all"])
+@pytest.mark.parametrize("pages", [8192, 8193, 40001])
+def test_fork_in_pools_of_many_pages(gpu, pages, free, in_place):
+    """Free pages far behind, too few of them, and none."""
+    announce(f"fork_pages {pages} pages, free: {free}")
+    rng = np.random.default_rng(pages)
+    refs = {"none": np.ones(pages, int), "last": (np.arange(pages) < pages - 5) * 2,
+            "some": (rng.random(pages) > 0.0005) * 1, "all": np.zeros(pages, int)}[free]
+    table = rng.integers(0, pages, (60, 3))
+    lens = np.where(np.arange(60) % 3 == 0, rng.integers(1, 190, 60), 0)
+    parents = np.where(lens == 0, np.arange(60) // 3 * 3, -1)
+    fork(gpu, table, lens, parents, refs, in_place)
+
+
+@pytest.mark.parametrize("requests,columns", [(128, 64), (129, 64), (3, 5000)])
+def test_release_and_compact_at_the_small_pools_limit(gpu, requests, columns):
+    announce(f"release_pages, compact_pages table of {requests} x {columns}")
+    table, lens, refs = make_pool(31, requests, (columns - 1) * 64, 10, idle=1, extra_columns=1)
+    assert table.shape[1] == columns
+    ended = (np.arange(requests) % 4 == 0) * 1
+    a, r = dev(lens), dev(refs)
+    gpu.release_pages(dev(table), a, dev(ended), r, a, r)
+    lens, refs = P.release(table.tolist(), lens.tolist(), ended.tolist(), refs.tolist())
+    same(a, lens)
+    same(r, refs)
+    t, src, dst, counts = dev(table), torch.empty_like(r), torch.empty_like(r), torch.empty(2, **I32)
+    gpu.compact_pages(t, a, r, t, r, src, dst, counts)
+    for got, w in zip((t, r, src, dst, counts), P.compact(table.tolist(), lens, refs)):
+        same(got, w)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("requests,longest,spare,idle", POOLS)
 def test_compact(gpu, requests, longest, spare, idle, in_place):
     announce(f"compact_pages {requests} requests in_place={in_place}")
