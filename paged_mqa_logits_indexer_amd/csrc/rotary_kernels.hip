@@ -6,14 +6,15 @@
 // Two bits per angle give its axis.  All layers of a model turn by the same angles,
 // so axis_rotations gathers them once a step, [tokens][64], and the appends take
 // that table with position t for token t; the queries' kernels gather for
-// themselves, once per token and thread, and turn several heads with it.
+// themselves, once per token and workgroup.
 //
 //   rotate_queries        64 dimensions of every (row, head), 16 bits in and out,
 //                         from and to strided places
 //   rotate_index_queries  the first 64 of 128 dimensions; all of them to E4M3 codes,
 //                         clamped to +-448, which indexer_logits reads
 //
-// Each value is rounded once (rotary.h).  Bound by memory.
+// Each value is rounded once (rotary.h).  Bound by memory: 4096 rows of 128 heads, of
+// 384 and 1152 bytes apart, move 134 MB in 34 us (3.9 TB/s; three axes 38 us).
 #include "indexer_common.h"
 #include "launches.h"
 #include "rotary.h"
@@ -44,23 +45,6 @@ __device__ __forceinline__ const float* angle_row(const RotaryArgs& a, const Axi
   return a.rope + static_cast<int64_t>(at) * kRope;
 }
 
-// factors_of for positions on several axes.
-__device__ __forceinline__ Factors gather_factors(const RotaryArgs& a, int token, int piece) {
-  const AxisPositions p = axis_positions(a, token);
-  if (a.axes == 1) return factors_of(piece, a.interleaved != 0, a.rope + static_cast<int64_t>(p.at[0]) * kRope);
-  Factors f;
-  const int first = a.interleaved ? 4 * piece : 8 * (piece & 3);
-  const float sign = a.interleaved || piece < 4 ? 1.0f : -1.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int angle = first + (a.interleaved ? i & 3 : i);
-    const float* row = angle_row(a, p, angle);
-    f.c[i] = row[angle];
-    f.s[i] = sign * row[kHalfRope + angle];
-  }
-  return f;
-}
-
 // 16 threads per token, four values each.
 __global__ __launch_bounds__(kThreads) void axis_rotations_kernel(RotaryArgs a) {
   const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
@@ -83,62 +67,56 @@ __device__ __forceinline__ int2 clamped_codes(F32Row x) {
   return e4m3_codes(x.v);
 }
 
-// 8 threads per (token, head), each with 8 rotated dimensions and, of an index query,
-// 8 of the others (the rotation, in float64, then keeps whole waves busy: with 16
-// threads, of which half rotate, 4001 rows of 32 heads 17.8 us instead of 13.7).  A
-// thread asks for AT heads before it turns the first, so that the chain position,
-// table row, factors stands beside them (4096 rows of 128 heads 45 -> 33 us).
-template <int DT, bool INDEX, int AT>
-__global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a, int chunks) {
-  constexpr int kBytes = DT == IDX_FP32 ? 4 : 2, kPiece = 8 * kBytes;
-  constexpr int kPieces = 8, kHeadsPerPass = kThreads / kPieces;
-  const int token = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int piece = threadIdx.x % kPieces;
-  const char* in = static_cast<const char*>(a.x) + static_cast<int64_t>(token) * a.x_token_stride * kBytes + piece * kPiece;
-  F32Row x[AT], other[AT], plain[INDEX ? AT : 1];
-  const int head0 = chunk * AT * kHeadsPerPass + static_cast<int>(threadIdx.x) / kPieces;
-#pragma unroll
-  for (int k = 0; k < AT; ++k) {
-    const int head = head0 + k * kHeadsPerPass;
-    if (head >= a.heads) continue;
-    const char* row = in + head * a.x_head_stride * kBytes;
-    x[k] = load8<DT>(row);
-    if (!a.interleaved) other[k] = load8<DT>(row + ((piece ^ 4) - piece) * kPiece);
-    if constexpr (INDEX) plain[k] = load8<DT>(row + kPieces * kPiece);
-  }
-  const Factors f = gather_factors(a, token, piece);
-#pragma unroll
-  for (int k = 0; k < AT; ++k) {
-    const int head = head0 + k * kHeadsPerPass;
-    if (head >= a.heads) continue;
-    turn8<INDEX ? IDX_FP32 : DT>(x[k], other[k], a.interleaved != 0, f);
-    if constexpr (INDEX) {
-      int2* out = static_cast<int2*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * (2 * kPieces) + piece;
-      out[0] = clamped_codes(x[k]);
-      out[kPieces] = clamped_codes(plain[k]);
-    } else {
-      // (in place: a row's 8 threads are of one wave, which has read its rows by now)
-      char* out = static_cast<char*>(a.out) +
-                  (static_cast<int64_t>(token) * a.out_token_stride + head * a.out_head_stride) * kBytes;
-      reinterpret_cast<i32x4*>(out)[piece] = pack16<DT>(x[k]);
-    }
-  }
-}
+// A workgroup per 32 heads of a token, 8 threads per head, each with 8 rotated
+// dimensions and, of an index query, 8 of the others (with 16 threads, of which half
+// rotate in float64, 4001 rows of 32 heads 17.8 us instead of 13.7).  The angles are
+// read from the table, or, on several axes, gathered in LDS by 64 threads (each thread
+// its own: 4096 rows of 128 heads 58 us instead of 38).  The queries are asked for
+// first, beside the chain position, table row, angles.  What is written goes past the
+// caches (38 instead of 40 us); several heads per thread measured 40 and 41 us.
+constexpr int kHeadsPerWg = kThreads / 8;
 
-template <int DT, bool INDEX, int AT>
-void launch_at(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev) {
-  constexpr int kHeads = AT * kThreads / 8;
-  const int chunks = (a.heads + kHeads - 1) / kHeads;
-  launch_kernel(rotate_kernel<DT, INDEX, AT>, dim3(static_cast<uint32_t>(a.tokens) * chunks), dim3(kThreads), stream,
-                ev.start, ev.stop, a, chunks);
+template <int DT, bool INDEX>
+__global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a, int chunks) {
+  constexpr int kBytes = DT == IDX_FP32 ? 4 : 2, kPiece = 8 * kBytes, kPieces = kRope / 8;
+  __shared__ __attribute__((aligned(16))) float s_row[kRope];
+  const int token = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  const int piece = threadIdx.x % kPieces, head = chunk * kHeadsPerWg + static_cast<int>(threadIdx.x) / kPieces;
+  const bool here = head < a.heads;
+  const char* row = static_cast<const char*>(a.x) +
+                    (static_cast<int64_t>(token) * a.x_token_stride + head * a.x_head_stride) * kBytes;
+  F32Row x{}, other{}, plain{};
+  if (here) {
+    x = load8<DT>(row + piece * kPiece);
+    if (!a.interleaved) other = load8<DT>(row + (piece ^ 4) * kPiece);
+    if constexpr (INDEX) plain = load8<DT>(row + (piece + kPieces) * kPiece);
+  }
+  const AxisPositions p = axis_positions(a, token);
+  const float* table = a.rope + static_cast<int64_t>(p.at[0]) * kRope;
+  if (a.axes > 1) {
+    if (threadIdx.x < kRope) s_row[threadIdx.x] = angle_row(a, p, threadIdx.x % kHalfRope)[threadIdx.x];
+    __syncthreads();
+    table = s_row;
+  }
+  if (!here) return;
+  turn8<INDEX ? IDX_FP32 : DT>(x, other, a.interleaved != 0, factors_of(piece, a.interleaved != 0, table));
+  if constexpr (INDEX) {
+    int2* out = static_cast<int2*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * (2 * kPieces) + piece;
+    out[0] = clamped_codes(x);
+    out[kPieces] = clamped_codes(plain);
+  } else {
+    // (in place: a row's 8 threads are of one wave, which has read the row by now)
+    char* out = static_cast<char*>(a.out) +
+                (static_cast<int64_t>(token) * a.out_token_stride + head * a.out_head_stride) * kBytes;
+    __builtin_nontemporal_store(pack16<DT>(x), reinterpret_cast<i32x4*>(out) + piece);
+  }
 }
 
 template <int DT, bool INDEX>
 void launch_rotate(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev) {
-  if constexpr (!INDEX) {
-    if (a.tokens >= 1024 && a.heads > kThreads / 8) return launch_at<DT, INDEX, 4>(a, stream, ev);
-  }
-  launch_at<DT, INDEX, 1>(a, stream, ev);
+  const int chunks = (a.heads + kHeadsPerWg - 1) / kHeadsPerWg;
+  launch_kernel(rotate_kernel<DT, INDEX>, dim3(static_cast<uint32_t>(a.tokens) * chunks), dim3(kThreads), stream,
+                ev.start, ev.stop, a, chunks);
 }
 
 }  // namespace
