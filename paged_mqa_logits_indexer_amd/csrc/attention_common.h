@@ -266,7 +266,7 @@ __device__ __forceinline__ Item make_item(const AttentionArgs& a, int id) {
     it.row0 = row;
     it.pair0 = t * M;
     it.pairs = min(M, a.heads - it.pair0);
-    it.tiles = (a.k + kTile - 1) / kTile;
+    it.tiles = a.row_lens ? a.row_lens[row] : (a.k + kTile - 1) / kTile;  // counted, or the whole list
     if (a.cu_q) {
       // the last request that starts at or before the row
       int lo = 0, hi = a.requests;
@@ -388,7 +388,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   const int tid = threadIdx.x;
   s.cost = kItemCost<M>;
   if constexpr (KIND == kSparse) {
-    if (!a.cu_q) {
+    if (!a.cu_q && !a.row_lens) {
       if (min_units == 0) s.cost = 0;
       const int n = (a.k + kTile - 1) / kTile + s.cost;
       s.total = static_cast<int64_t>(items) * n;
@@ -619,6 +619,10 @@ __global__ __launch_bounds__(256) void join_shared_kernel(JoinArgs a, int M, int
   write_joined<DT>(j, pair, a.out, a.lse);
 }
 
+// The workspace's last part: an int for each row of a selection (attention over 4-bit
+// rows counts the tiles of a list that hold a key).
+constexpr size_t kRowCountBytes = 65536 * sizeof(int32_t);
+
 constexpr int kMaxGrid = 256;  // one persistent workgroup per CU
 constexpr int kMinTiles = 2;   // smallest part of an item that is cut into equal ones
 template <int M>
@@ -675,7 +679,7 @@ hipError_t launch_joined(void (*kernel)(AttentionArgs, int, JoinInfo*, float*), 
   int grid = static_cast<int>(
       std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + kItemCost<M>) / kMinUnits<M>)));
   int min_units = kMinUnits<M>;
-  if (KIND == kSparse && !a.cu_q && items <= kMaxGrid / 2) {  // parts of one item each
+  if (KIND == kSparse && !a.cu_q && !a.row_lens && items <= kMaxGrid / 2) {  // parts of one item each
     grid = static_cast<int>(items * std::min<int64_t>(kMaxGrid / items, std::max<int64_t>(1, tiles / kMinTiles)));
     min_units = 0;
   }
