@@ -375,7 +375,7 @@ __global__ __launch_bounds__(256) void count_tiles_kernel(const int32_t* __restr
   const int row = blockIdx.x * 4 + static_cast<int>(threadIdx.x) / kWave, lane = lane_id();
   if (row >= rows) return;
   const int32_t* list = indices + static_cast<int64_t>(row) * k;
-  constexpr int kAt = 4;  // loads in flight
+  constexpr int kAt = 16;  // loads in flight
   int last = 0;
   for (int end = k; end > 0 && last == 0; end -= kAt * kWave) {
     int tok[kAt];

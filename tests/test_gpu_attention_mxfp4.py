@@ -8,6 +8,7 @@ import torch
 
 import oracle as O
 import tests.test_gpu_attention as base
+import tests.test_gpu_attention_limits as limits
 import tests.test_gpu_attention_range as ranges
 import tests.test_gpu_attention_rms as rms
 from tests.gpu_harness import DEV, announce
@@ -64,6 +65,23 @@ def test_as_16_bit_rms(four, test, case):
     test(four, **case)
 
 
+@pytest.mark.parametrize("case", ["selections", "pages of 1 head", "pages of 17 heads"])
+def test_as_16_bit_most_rows(gpu, monkeypatch, case):
+    """As many rows and requests as a call takes."""
+    announce(f"4-bit rows: most rows, {case}")
+    plain = limits.caches
+
+    def rounded(*args):
+        g, cache, table = plain(*args)
+        return g, unpack(pack(cache), cache.dtype), table
+
+    monkeypatch.setattr(limits, "caches", rounded)
+    if case == "selections":
+        limits.test_most_ragged_rows_over_selections(Packing(gpu))
+    else:
+        limits.test_most_requests_over_pages(Packing(gpu), int(case.split()[2]), 15)
+
+
 def test_packing_is_the_oracles(gpu):
     announce("packing of the tests")
     x = torch.randn(50, 576, generator=torch.Generator().manual_seed(1)).bfloat16()
@@ -79,7 +97,8 @@ def test_packing_is_the_oracles(gpu):
 
 @pytest.mark.parametrize("form", ["paged", "shared", "sparse"])
 @pytest.mark.parametrize("heads", [16, 32, 64, 128])
-@pytest.mark.parametrize("dtype,powers", [("bf16", (0, 1, 3, 60, 127, 200, 240)), ("fp16", (101, 103, 110, 127, 138, 140))])
+@pytest.mark.parametrize("dtype,powers", [("bf16", (0, 1, 3, 60, 127, 200, 240)),
+                                          ("fp16", (101, 103, 110, 127, 138, 140))])
 def test_powers_of_two_at_both_ends(gpu, dtype, powers, heads, form):
     """Every code under powers from the least to nearly the largest that stay in the
     type, one power a request; the queries see the latent part through the rotated
@@ -121,7 +140,8 @@ def test_powers_of_two_at_both_ends(gpu, dtype, powers, heads, form):
     torch.cuda.synchronize()
     values = L.latent_mxfp4_values(rows.view(-1, 400).numpy(), dtype)
     if dtype == "fp16":  # keys are taken in the queries' type, which holds 2^-25 (a power below 104) rounded
-        values = values.astype(np.float16).astype(np.float64)
+        with np.errstate(over="ignore"):
+            values = values.astype(np.float16).astype(np.float64)
     for i, k in enumerate(lens):
         s = np.arange(k)
         keys = values[table[i, s // 64].astype(np.int64) * 64 + s % 64]
@@ -162,8 +182,14 @@ def test_far_pages(gpu):
     cache = torch.zeros(pages, 64, 400, dtype=torch.uint8, device=DEV)
     g = torch.Generator().manual_seed(9)
     table = torch.tensor([[pages - 1, pages - 200, 3, pages - 9]], dtype=torch.int32)
-    rows = pack(torch.randn(4, 64, 576, generator=g).bfloat16())
-    cache[table[0].long().to(DEV)] = rows.to(DEV)
+    plain = torch.randn(4, 64, 576, generator=g).bfloat16()
+    rows = pack(plain)
+    # written by the append, at the position whose angles are zero
+    slots = (table[0][:, None] * 64 + torch.arange(64)).flatten().int()
+    at = torch.zeros(256, dtype=torch.int32, device=DEV)
+    still = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).to(DEV)
+    gpu.latent_append_mxfp4(plain.view(256, 576).to(DEV), at, slots.to(DEV), still, cache)
+    assert torch.equal(cache[table[0].long().to(DEV)].cpu(), rows)
     keys = L.latent_mxfp4_values(rows.view(-1, 400).numpy(), "bf16")
     for heads in (16, 128):
         q = torch.randn(1, heads, 576, generator=g).bfloat16()
@@ -181,6 +207,58 @@ def test_far_pages(gpu):
             torch.cuda.synchronize()
             assert (np.abs(out[0].double().cpu().numpy() - want) <= ob).all()
             assert (np.abs(lse[0].double().cpu().numpy() - wl) <= lb).all()
+
+
+@pytest.mark.parametrize("heads", [16, 64, 128])
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 1e-30])
+def test_scales(four, heads, scale):
+    """A factor that turns the scores' order round, and ones that make them all alike."""
+    announce(f"attention mxfp4 scale={scale} heads={heads}")
+    b = Batch4(151, heads, [1] * 4, [300, 65, 1, 900], width=600)
+    lists = np.full((4, 960), -1, np.int32)
+    for r, n in enumerate(b.ends):
+        lists[r, :n] = np.arange(n)
+    q, rows, table = b.q.to(DEV), b.cache.to(DEV), b.dev(b.table)
+    for call, keys in (("paged_attention", b.ends.astype(np.int32)), ("sparse_attention", lists)):
+        out, lse = b.out()
+        getattr(four, call)(q, rows, table, b.dev(keys), 1, scale, out, lse)
+        torch.cuda.synchronize()
+        for r, n in enumerate(b.ends):
+            at = np.arange(n)
+            keys_r = b.cache.view(-1, 576)[torch.from_numpy(b.slots(r, at))].double().numpy()
+            want, wl, ob, lb = L.attend_row(b.q[r].double().numpy(), keys_r, at, scale)
+            assert (np.abs(out[r].double().cpu().numpy() - want) <= ob + n * 2.0 ** -110 * 8).all()
+            assert (np.abs(lse[r].double().cpu().numpy() - wl) <= lb).all()
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("heads,rows,k", [(16, 300, 700), (32, 300, 700), (64, 300, 5000), (128, 200, 2300)])
+def test_padded_selections_of_many(gpu, heads, rows, k, ragged):
+    """Selections that are counted before they are shared out: full lists, lists that end
+    early, one key at either end, keys behind long padding, none."""
+    announce(f"sparse_attention_mxfp4 padded heads={heads} rows={rows} k={k}")
+    counts = [rows // 3, 0, rows - rows // 3] if ragged else [rows]
+    b = Batch4(161, heads, counts, np.full(rows, 6000))
+    rng = np.random.default_rng(k)
+    lists, picked = np.full((rows, k), -1, np.int32), []
+    for r in range(rows):
+        kind, n = r % 7, int(rng.integers(1, 200))
+        places = {0: np.arange(k), 1: np.arange(n), 2: [0], 3: [k - 1], 4: np.arange(k - n, k), 5: [],
+                  6: np.sort(rng.permutation(k)[:n])}[kind]
+        chosen = rng.permutation(6000)[:len(places)]
+        lists[r, np.asarray(places, int)] = chosen
+        if kind != 0:
+            holes = np.setdiff1d(np.arange(k), places)
+            lists[r, holes] = rng.choice([-1, b.max_pages * 64, 2 ** 31 - 1, -2 ** 31], len(holes))
+        picked.append(chosen)
+    out, lse = b.out()
+    gpu.sparse_attention_mxfp4(b.q.to(DEV), pack(b.cache).to(DEV), b.dev(b.table), b.dev(lists), 0 if ragged else rows,
+                               SCALE, out, lse, cu_q=b.dev(b.first.astype(np.int32)) if ragged else None)
+    torch.cuda.synchronize()
+    b.check(out, lse, picked=picked, rows=list(range(14)) + [rows // 3 - 1, rows // 3, rows - 7, rows - 6, rows - 5,
+                                                             rows - 4, rows - 3, rows - 2, rows - 1])
+    some = torch.tensor([len(p) > 0 for p in picked])
+    assert torch.isfinite(lse.cpu()[some]).all() and (lse.cpu()[~some] == -torch.inf).all()
 
 
 def all_calls(gpu, b, prefix, workspace=None):
@@ -201,7 +279,8 @@ def test_graphs_share_a_workspace(gpu, heads):
     """Two captured graphs with one workspace, replayed in turn with eager calls in
     between: every replay gives the eager bits."""
     announce(f"attention mxfp4 graphs heads={heads}")
-    batches = [base.Batch(111 + i, heads, [1] * 5, [128 + 900 * i, 140, 700, 129, 2000 - i], shared=2) for i in range(2)]
+    batches = [base.Batch(111 + i, heads, [1] * 5, [128 + 900 * i, 140, 700, 129, 2000 - i], shared=2)
+               for i in range(2)]
     need = max(gpu.attention_workspace_bytes(5, heads, 5), gpu.shared_prefix_workspace_bytes(5, heads, 5))
     ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(0xA5)
     graphs = []
@@ -319,7 +398,8 @@ def test_serving_chain(gpu):
     rows_at = L.axis_rows(rope.numpy(), axes.numpy(), axis_of)
     want_q = L.rotate(ql[:, :, 512:].double().numpy(), rows_at[last.numpy()][:, None], False)
     assert (np.abs(q[:, :, 512:].double().cpu().numpy() - want_q) <= 2.0 ** -8 * np.abs(want_q) + 2.0 ** -40).all()
-    assert np.array_equal(q8.cpu().numpy(), L.e4m3_codes(L.index_key(qi.float().numpy(), rows_at[last.numpy()][:, None], False)))
+    want_qi = L.index_key(qi.float().numpy(), rows_at[last.numpy()][:, None], False)
+    assert np.array_equal(q8.cpu().numpy(), L.e4m3_codes(want_qi))
     want_idx = O.topk_rows(logits.cpu().numpy(), np.array(lens[:3]), k, O.KEY_FP32)
 
     def check(got, got_lse, cache, tab, r, query, chosen):
