@@ -113,7 +113,7 @@ __device__ __attribute__((aligned(128))) const uint32_t kZeroRow[IDX_LATENT_ROW 
 
 // 16-byte chunks of a key's 128 bytes are exchanged by c ^ swz(key) in LDS, which
 // spreads the K operand's 128-bit reads and V's transposing 64-bit reads over all
-// banks (attention_kernels.hip).
+// banks (attention_tiles.h).
 __device__ __forceinline__ int swz(int key) { return (((key >> 1) & 1) << 2) | (-(key >> 2) & 3); }
 // Keys that are written to LDS from registers (MX) also exchange by their last bit:
 // eight lanes that write the same chunk of eight keys then take all 32 banks of a
