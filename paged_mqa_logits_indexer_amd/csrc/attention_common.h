@@ -363,8 +363,7 @@ struct Share {
 // ragged extends and 8 requests on a shared prefix with 6 instead of 3.)
 template <int M>
 constexpr int kItemCost = M == 128 ? 6 : 3;
-template <int M>
-__device__ __forceinline__ int item_units(const Item& it) { return it.tiles ? it.tiles + kItemCost<M> : 0; }
+__device__ __forceinline__ int item_units(const Item& it, int cost) { return it.tiles ? it.tiles + cost : 0; }
 
 // Share of workgroup w of a grid: equal parts [w, w + 1) / groups of the units,
 // of as many groups as have min_units each.
@@ -381,12 +380,13 @@ __device__ __forceinline__ int share_owner(int64_t total, int groups, int64_t t)
 
 // min_units 0 (sparse lists of few rows): every item is cut into grid / items
 // equal parts, so that a workgroup has one of them, and items cost nothing.
-template <int KIND, int M, int THREADS>
+// COST: what an item counts for beside its tiles.
+template <int KIND, int M, int THREADS, int COST = kItemCost<M>>
 __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_units, int* s_scan, int64_t* s_res) {
   Share s;
   const int items = static_cast<int>(item_count<KIND, M>(a));
   const int tid = threadIdx.x;
-  s.cost = kItemCost<M>;
+  s.cost = COST;
   if constexpr (KIND == kSparse) {
     if (!a.cu_q && !a.row_lens) {
       if (min_units == 0) s.cost = 0;
@@ -404,7 +404,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   }
   if (items <= kWave) {
     // few items: every wave by itself, an item per lane
-    const int n = lane_id() < items ? item_units<M>(make_item<KIND, M, 1>(a, lane_id())) : 0;
+    const int n = lane_id() < items ? item_units(make_item<KIND, M, 1>(a, lane_id()), COST) : 0;
     const int upto = wave_inclusive_scan(n);
     s.total = __builtin_amdgcn_readlane(upto, kWave - 1);
     s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_units)));
@@ -422,7 +422,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   int n = 0;
   for (int c = 0; c < chunks; ++c) {
     const int id = c * THREADS + tid;
-    n = id < items ? item_units<M>(make_item<KIND, M, 1>(a, id)) : 0;
+    n = id < items ? item_units(make_item<KIND, M, 1>(a, id), COST) : 0;
     const int sum = wave_sum(n);
     if (lane_id() == 0) s_wave[tid / kWave] = sum;
     __syncthreads();
@@ -450,7 +450,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   int c = 0;
   while (c + 1 < chunks && at + s_chunk[c] <= s.t0) at += s_chunk[c++];
   const int id = c * THREADS + tid;
-  if (c + 1 < chunks) n = id < items ? item_units<M>(make_item<KIND, M, 1>(a, id)) : 0;
+  if (c + 1 < chunks) n = id < items ? item_units(make_item<KIND, M, 1>(a, id), COST) : 0;
   const int upto = wave_inclusive_scan(n);
   if (lane_id() == kWave - 1) s_wave[tid / kWave] = upto;
   __syncthreads();
@@ -671,13 +671,17 @@ int tile_pairs(const AttentionArgs& a, const double (&per_tile)[4], const double
 }
 
 // One attention kernel over shares of the work list, and the join of what it split.
-template <int DT, int KIND, int M>
+template <int DT, int KIND, int M, int COST = kItemCost<M>>
 hipError_t launch_joined(void (*kernel)(AttentionArgs, int, JoinInfo*, float*), int threads, const AttentionArgs& a,
                          hipStream_t stream, LaunchEvents ev) {
   const int64_t items = item_count<KIND, M>(a);
   const int64_t tiles = KIND == kSparse ? (a.k + kTile - 1) / kTile : a.max_pages;
   int grid = static_cast<int>(
-      std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + kItemCost<M>) / kMinUnits<M>)));
+      std::max(int64_t{1}, std::min(int64_t{kMaxGrid}, items * (tiles + COST) / kMinUnits<M>)));
+  // One item of a few tiles stays whole and needs no join, also where it counts for more
+  // than the smallest share: one request of 65 keys 12.2 us in two parts, 10.5 in one.
+  // (64 such requests on 64 workgroups 21.2 us, on 121 16.4.)
+  if (items == 1) grid = static_cast<int>(std::min<int64_t>(grid, std::max<int64_t>(1, tiles / kMinTiles)));
   int min_units = kMinUnits<M>;
   if (KIND == kSparse && !a.cu_q && !a.row_lens && items <= kMaxGrid / 2) {  // parts of one item each
     grid = static_cast<int>(items * std::min<int64_t>(kMaxGrid / items, std::max<int64_t>(1, tiles / kMinTiles)));

@@ -43,7 +43,11 @@ __device__ __forceinline__ s16x8 finite_or_zero(s16x8 x) {
   return x;
 }
 
-constexpr int kOwnKeys = 16;                     // keys that a wave takes at a time
+// What taking up and writing a pair tile counts for in tiles, whose time here is short
+// (calls with 3, as in the other kernel, 6, 9 and 12: 64 requests of 1 .. 32768 keys 43 /
+// 36 / 36 / 36 us, of 64 keys 22 / 16 / 17 / 17, 256 of 1 .. 4096 keys 39 / 38 / 40 / 41).
+constexpr int kOwnCost = 8;
+constexpr int kOwnKeys = 16;                 // keys that a wave takes at a time
 constexpr int kOwnOctet = 8 * 1024;              // LDS image of 8 keys: their values alone
 constexpr int kOwnImage = 2 * kOwnOctet;
 constexpr int kQueryAt = kWaves * kOwnImage;     // behind the waves' images: the queries
@@ -68,7 +72,7 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
   // consecutive shares on one XCD (workgroups are dealt to the 8 XCDs in turn)
   const int w = (grid & 7) ? static_cast<int>(blockIdx.x)
                            : static_cast<int>(blockIdx.x & 7) * (grid >> 3) + static_cast<int>(blockIdx.x >> 3);
-  const Share share = find_share<KIND, M, kThreads>(a, w, grid, min_units, s_scan, s_res);
+  const Share share = find_share<KIND, M, kThreads, kOwnCost>(a, w, grid, min_units, s_scan, s_res);
   if (KIND != kShared && tid == 0) join[w].pieces = 0;
   if (share.t0 >= share.t1) return;
 
@@ -424,7 +428,7 @@ hipError_t launch(AttentionArgs a, hipStream_t stream, LaunchEvents ev) {
       ev.start = nullptr;
     }
   }
-  if constexpr (M == 16) return launch_joined<DT, KIND, M>(own_keys_kernel<DT, KIND>, kThreads, a, stream, ev);
+  if constexpr (M == 16) return launch_joined<DT, KIND, M, kOwnCost>(own_keys_kernel<DT, KIND>, kThreads, a, stream, ev);
   else return launch_joined<DT, KIND, M>(attention_kernel<DT, KIND, M, true>, kAttnThreads, a, stream, ev);
 }
 
