@@ -19,10 +19,10 @@
 // keys 97 instead of 56.)
 //
 // Measured (MI355X; kernels, medians under the kernel trace): 64 requests of 1 .. 32768
-// keys with 16 heads 37 us (85 MB of keys; over 16 bits 54); calls: 64 requests of 32768
+// keys with 16 heads 33.5 us (85 MB of keys; over 16 bits 54); calls: 64 requests of 32768
 // keys 200 us (839 MB, 4.2 TB/s; over 16 bits 402), 16 requests of 32768 keys with 128
 // heads 195 us (749 TFLOP/s; over 16 bits 195), 512 rows of 128 heads over 2048 listed
-// keys 358 us (816 TFLOP/s; 358), one request of 65 keys 10.4 us.  With few heads the K
+// keys 358 us (816 TFLOP/s; 358), one request of 65 keys 10.5 us.  With few heads the K
 // stream bounds it, with many the MFMAs and what stands between them, as over 16 bits;
 // unpacking is 0 to 5 % of the wide form's time.
 #include "attention_tiles.h"
