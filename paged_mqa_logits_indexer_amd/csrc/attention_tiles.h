@@ -356,7 +356,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
       if (part == 0) packed[0].codes[0] = __builtin_bit_cast(i32x4, lds_read(at)), packed[0].power[0] = lds_read_byte(power);
       if (part == 1)
         packed[0].codes[1] = __builtin_bit_cast(i32x4, lds_read(at + 1024)), packed[0].power[1] = lds_read_byte(power + 8);
-      if (part == 2) packed[0].rotated = __builtin_bit_cast(i32x4, lds_read(at + 3072));
+      if (part == 2) packed[0].rotated = __builtin_bit_cast(i32x4, lds_read(at + 3 * 1024));
     };
     auto unpack = [&](uint32_t base, int step, int o, int j) {
       if (j < 8) {
