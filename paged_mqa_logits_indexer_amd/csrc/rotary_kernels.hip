@@ -74,13 +74,12 @@ __device__ __forceinline__ int2 clamped_codes(F32Row x) {
 // its own: 4096 rows of 128 heads 58 us instead of 38).  The queries are asked for
 // first, beside the chain position, table row, angles.  What is written goes past the
 // caches (38 instead of 40 us); several heads per thread measured 40 and 41 us.
-constexpr int kHeadsPerWg = kThreads / 8;
-
 template <int DT, bool INDEX>
-__global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a, int chunks) {
+__global__ __launch_bounds__(kRotateThreads) void rotate_kernel(RotaryArgs a, int chunks) {
   constexpr int kBytes = DT == IDX_FP32 ? 4 : 2, kPiece = 8 * kBytes, kPieces = kRope / 8;
   __shared__ __attribute__((aligned(16))) float s_row[kRope];
-  const int token = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  const int token = blockIdx.z * kSlabTokens + blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  if (token >= a.tokens) return;  // (whole workgroups of the last slab)
   const int piece = threadIdx.x % kPieces, head = chunk * kHeadsPerWg + static_cast<int>(threadIdx.x) / kPieces;
   const bool here = head < a.heads;
   const char* row = static_cast<const char*>(a.x) +
@@ -114,9 +113,9 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a, int chun
 
 template <int DT, bool INDEX>
 void launch_rotate(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev) {
-  const int chunks = (a.heads + kHeadsPerWg - 1) / kHeadsPerWg;
-  launch_kernel(rotate_kernel<DT, INDEX>, dim3(static_cast<uint32_t>(a.tokens) * chunks), dim3(kThreads), stream,
-                ev.start, ev.stop, a, chunks);
+  const RotateGrid grid = rotate_grid(a.tokens, a.heads);
+  launch_kernel(rotate_kernel<DT, INDEX>, dim3(grid.x, 1, grid.z), dim3(kRotateThreads), stream, ev.start, ev.stop, a,
+                grid.chunks);
 }
 
 }  // namespace
