@@ -255,7 +255,9 @@ __device__ __forceinline__ void key_range(const AttentionArgs& a, int r0, int r1
 // Item `id` of the list.  Dense: requests' pair tiles.  Shared: first the pair
 // tiles of the whole batch over the prefix pages, then the requests' pair
 // tiles over what follows.  Sparse: rows' pair tiles over the selection.
-template <int KIND, int M, int BY>
+// COUNTED: selections may come with the tiles of each row that hold a key
+// (row_lens); the 16-bit kernels do not look for them.
+template <int KIND, int M, int BY, bool COUNTED = false>
 __device__ __forceinline__ Item make_item(const AttentionArgs& a, int id) {
   const int capacity = a.max_pages * kPage;
   Item it{};
@@ -266,7 +268,8 @@ __device__ __forceinline__ Item make_item(const AttentionArgs& a, int id) {
     it.row0 = row;
     it.pair0 = t * M;
     it.pairs = min(M, a.heads - it.pair0);
-    it.tiles = a.row_lens ? a.row_lens[row] : (a.k + kTile - 1) / kTile;  // counted, or the whole list
+    it.tiles = (a.k + kTile - 1) / kTile;
+    if (COUNTED && a.row_lens) it.tiles = a.row_lens[row];
     if (a.cu_q) {
       // the last request that starts at or before the row
       int lo = 0, hi = a.requests;
@@ -381,14 +384,14 @@ __device__ __forceinline__ int share_owner(int64_t total, int groups, int64_t t)
 // min_units 0 (sparse lists of few rows): every item is cut into grid / items
 // equal parts, so that a workgroup has one of them, and items cost nothing.
 // COST: what an item counts for beside its tiles.
-template <int KIND, int M, int THREADS, int COST = kItemCost<M>>
+template <int KIND, int M, int THREADS, int COST = kItemCost<M>, bool COUNTED = false>
 __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_units, int* s_scan, int64_t* s_res) {
   Share s;
   const int items = static_cast<int>(item_count<KIND, M>(a));
   const int tid = threadIdx.x;
   s.cost = COST;
   if constexpr (KIND == kSparse) {
-    if (!a.cu_q && !a.row_lens) {
+    if (!a.cu_q && !(COUNTED && a.row_lens)) {
       if (min_units == 0) s.cost = 0;
       const int n = (a.k + kTile - 1) / kTile + s.cost;
       s.total = static_cast<int64_t>(items) * n;
@@ -404,7 +407,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   }
   if (items <= kWave) {
     // few items: every wave by itself, an item per lane
-    const int n = lane_id() < items ? item_units(make_item<KIND, M, 1>(a, lane_id()), COST) : 0;
+    const int n = lane_id() < items ? item_units(make_item<KIND, M, 1, COUNTED>(a, lane_id()), COST) : 0;
     const int upto = wave_inclusive_scan(n);
     s.total = __builtin_amdgcn_readlane(upto, kWave - 1);
     s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), s.total / min_units)));
@@ -422,7 +425,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   int n = 0;
   for (int c = 0; c < chunks; ++c) {
     const int id = c * THREADS + tid;
-    n = id < items ? item_units(make_item<KIND, M, 1>(a, id), COST) : 0;
+    n = id < items ? item_units(make_item<KIND, M, 1, COUNTED>(a, id), COST) : 0;
     const int sum = wave_sum(n);
     if (lane_id() == 0) s_wave[tid / kWave] = sum;
     __syncthreads();
@@ -450,7 +453,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   int c = 0;
   while (c + 1 < chunks && at + s_chunk[c] <= s.t0) at += s_chunk[c++];
   const int id = c * THREADS + tid;
-  if (c + 1 < chunks) n = id < items ? item_units(make_item<KIND, M, 1>(a, id), COST) : 0;
+  if (c + 1 < chunks) n = id < items ? item_units(make_item<KIND, M, 1, COUNTED>(a, id), COST) : 0;
   const int upto = wave_inclusive_scan(n);
   if (lane_id() == kWave - 1) s_wave[tid / kWave] = upto;
   __syncthreads();

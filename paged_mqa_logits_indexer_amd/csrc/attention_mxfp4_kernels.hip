@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
   // consecutive shares on one XCD (workgroups are dealt to the 8 XCDs in turn)
   const int w = (grid & 7) ? static_cast<int>(blockIdx.x)
                            : static_cast<int>(blockIdx.x & 7) * (grid >> 3) + static_cast<int>(blockIdx.x >> 3);
-  const Share share = find_share<KIND, M, kThreads, kOwnCost>(a, w, grid, min_units, s_scan, s_res);
+  const Share share = find_share<KIND, M, kThreads, kOwnCost, true>(a, w, grid, min_units, s_scan, s_res);
   if (KIND != kShared && tid == 0) join[w].pieces = 0;
   if (share.t0 >= share.t1) return;
 
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
   int64_t item_at = share.item_at;
   int item = share.item;
   for (; at < share.t1 && item < items; ++item) {
-    const Item it = make_item<KIND, M, kWave>(a, item);
+    const Item it = make_item<KIND, M, kWave, true>(a, item);
     const int64_t tiles_at = item_at + (it.tiles ? share.cost : 0);
     item_at = tiles_at + it.tiles;
     const int lo = static_cast<int>(max(int64_t{0}, at - tiles_at));

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   // consecutive shares on one XCD (workgroups are dealt to the 8 XCDs in turn)
   const int w = (grid & 7) ? static_cast<int>(blockIdx.x)
                            : static_cast<int>(blockIdx.x & 7) * (grid >> 3) + static_cast<int>(blockIdx.x >> 3);
-  const Share share = find_share<KIND, M, kAttnThreads>(a, w, grid, min_units, s_scan, s_res);
+  const Share share = find_share<KIND, M, kAttnThreads, kItemCost<M>, MX>(a, w, grid, min_units, s_scan, s_res);
   if (KIND != kShared && tid == 0) join[w].pieces = 0;
   if (share.t0 >= share.t1) return;
 
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   int64_t item_at = share.item_at;
   int item = share.item;
   for (; at < share.t1 && item < items; ++item) {
-    const Item it = make_item<KIND, M, kWave>(a, item);
+    const Item it = make_item<KIND, M, kWave, MX>(a, item);
     const int64_t tiles_at = item_at + (it.tiles ? share.cost : 0);
     item_at = tiles_at + it.tiles;
     const int lo = static_cast<int>(max(int64_t{0}, at - tiles_at));
