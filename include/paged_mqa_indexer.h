@@ -709,7 +709,7 @@ idx_status copy_pages(void* const* caches, const int32_t* token_bytes, int32_t n
  * out          (device) [rows][heads][512] of q's type, 16-B aligned
  * lse          (device) float [rows][heads], or NULL
  * workspace    (device) scratch of at least attention_workspace_bytes(rows,
- *              heads, requests) bytes (at most 136 MB), 256-B aligned; needs no
+ *              heads, requests) bytes (at most 135 MB), 256-B aligned; needs no
  *              initialisation.  Calls that share a workspace must be ordered on one stream.
  * Errors: IDX_EINVAL (NULL pointer, non-positive size, next_n and cu_q both or
  * neither, rows != requests * next_n, scale or softcap), IDX_EUNSUPPORTED

@@ -252,11 +252,47 @@ __device__ __forceinline__ void key_range(const AttentionArgs& a, int r0, int r1
   it.tiles = (hi + kTile - 1) / kTile - it.tile0;
 }
 
+// What the join kernel needs to know of a pair tile that several workgroups
+// share: written by the workgroup that holds the tile's beginning.
+struct alignas(16) JoinInfo {
+  int first;      // the first workgroup with a part of it
+  int pieces;     // 0: nothing to join here
+  int pairs;
+  int pad;
+  int64_t pair0;  // first pair, counted over the whole batch
+  int64_t pad2;
+};
+
+constexpr int kMaxGrid = 256;  // one persistent workgroup per CU
+__host__ __device__ __forceinline__ size_t join_bytes(int64_t infos) {
+  return (static_cast<size_t>(infos) * sizeof(JoinInfo) + 255) / 256 * 256;
+}
+
+// Pieces in the workspace: float o[M][512], then float2 (m, l)[M].  Dense and
+// sparse: two per workgroup, for a pair tile that began before it (2 w) and one
+// that ends after it (2 w + 1).  Shared: every (workgroup, item) visit is a
+// piece, w + item -- consecutive over a pair tile's workgroups.
+__host__ __device__ __forceinline__ int64_t piece_floats(int m) { return static_cast<int64_t>(m) * (kValDim + 2); }
+
+// Counted selections: a byte for each row, its tiles (at most 128), where the pieces
+// would begin.  No pair tile began before the first workgroup and none ends after the
+// last, so two pieces are never written, the first and the last: counts take the
+// place of the first, and where that is too short for them (16 pairs), the pieces go
+// on behind them, up to the end of the last.
+constexpr int kCountBytes = 65536;
+__host__ __device__ __forceinline__ uint8_t* row_tiles(const AttentionArgs& a) {
+  return static_cast<uint8_t*>(a.workspace) + join_bytes(kMaxGrid);
+}
+constexpr int64_t piece_bytes(int m) { return static_cast<int64_t>(m) * (kValDim + 2) * sizeof(float); }
+constexpr int64_t counted_shift(int m) { return kCountBytes > piece_bytes(m) ? kCountBytes - piece_bytes(m) : 0; }
+static_assert(IDX_MAX_ROWS <= kCountBytes && (IDX_CANDIDATE_CAPACITY + kTile - 1) / kTile < 256, "a byte for each row");
+static_assert(counted_shift(16) <= piece_bytes(16) && counted_shift(16) % 16 == 0, "counts and pieces fit");
+
 // Item `id` of the list.  Dense: requests' pair tiles.  Shared: first the pair
 // tiles of the whole batch over the prefix pages, then the requests' pair
 // tiles over what follows.  Sparse: rows' pair tiles over the selection.
 // COUNTED: selections may come with the tiles of each row that hold a key
-// (row_lens); the 16-bit kernels do not look for them.
+// (row_tiles); the 16-bit kernels do not look for them.
 template <int KIND, int M, int BY, bool COUNTED = false>
 __device__ __forceinline__ Item make_item(const AttentionArgs& a, int id) {
   const int capacity = a.max_pages * kPage;
@@ -269,7 +305,7 @@ __device__ __forceinline__ Item make_item(const AttentionArgs& a, int id) {
     it.pair0 = t * M;
     it.pairs = min(M, a.heads - it.pair0);
     it.tiles = (a.k + kTile - 1) / kTile;
-    if (COUNTED && a.row_lens) it.tiles = a.row_lens[row];
+    if (COUNTED && a.counted) it.tiles = row_tiles(a)[row];
     if (a.cu_q) {
       // the last request that starts at or before the row
       int lo = 0, hi = a.requests;
@@ -391,7 +427,7 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   const int tid = threadIdx.x;
   s.cost = COST;
   if constexpr (KIND == kSparse) {
-    if (!a.cu_q && !(COUNTED && a.row_lens)) {
+    if (!a.cu_q && !(COUNTED && a.counted)) {
       if (min_units == 0) s.cost = 0;
       const int n = (a.k + kTile - 1) / kTile + s.cost;
       s.total = static_cast<int64_t>(items) * n;
@@ -468,23 +504,6 @@ __device__ Share find_share(const AttentionArgs& a, int w, int grid, int min_uni
   s.item_at = s_res[1];
   return s;
 }
-
-// What the join kernel needs to know of a pair tile that several workgroups
-// share: written by the workgroup that holds the tile's beginning.
-struct alignas(16) JoinInfo {
-  int first;      // the first workgroup with a part of it
-  int pieces;     // 0: nothing to join here
-  int pairs;
-  int pad;
-  int64_t pair0;  // first pair, counted over the whole batch
-  int64_t pad2;
-};
-
-// Pieces in the workspace: float o[M][512], then float2 (m, l)[M].  Dense and
-// sparse: two per workgroup, for a pair tile that began before it (2 w) and one
-// that ends after it (2 w + 1).  Shared: every (workgroup, item) visit is a
-// piece, w + item -- consecutive over a pair tile's workgroups.
-__host__ __device__ __forceinline__ int64_t piece_floats(int m) { return static_cast<int64_t>(m) * (kValDim + 2); }
 
 // What masks and the bias need to know of a pair; read when they do (the wide
 // form has no registers to keep it in).
@@ -622,16 +641,9 @@ __global__ __launch_bounds__(256) void join_shared_kernel(JoinArgs a, int M, int
   write_joined<DT>(j, pair, a.out, a.lse);
 }
 
-// The workspace's last part: an int for each row of a selection (attention over 4-bit
-// rows counts the tiles of a list that hold a key).
-constexpr size_t kRowCountBytes = 65536 * sizeof(int32_t);
-
-constexpr int kMaxGrid = 256;  // one persistent workgroup per CU
 constexpr int kMinTiles = 2;   // smallest part of an item that is cut into equal ones
 template <int M>
 constexpr int kMinUnits = kItemCost<M> + 2;  // smallest share: below, the join costs more than the split saves
-
-size_t join_bytes(int64_t infos) { return (static_cast<size_t>(infos) * sizeof(JoinInfo) + 255) / 256 * 256; }
 
 // Pairs that one request (sparse: one row; shared: the batch, for the prefix)
 // brings together.
@@ -686,13 +698,14 @@ hipError_t launch_joined(void (*kernel)(AttentionArgs, int, JoinInfo*, float*), 
   // (64 such requests on 64 workgroups 21.2 us, on 121 16.4.)
   if (items == 1) grid = static_cast<int>(std::min<int64_t>(grid, std::max<int64_t>(1, tiles / kMinTiles)));
   int min_units = kMinUnits<M>;
-  if (KIND == kSparse && !a.cu_q && !a.row_lens && items <= kMaxGrid / 2) {  // parts of one item each
+  if (KIND == kSparse && !a.cu_q && !a.counted && items <= kMaxGrid / 2) {  // parts of one item each
     grid = static_cast<int>(items * std::min<int64_t>(kMaxGrid / items, std::max<int64_t>(1, tiles / kMinTiles)));
     min_units = 0;
   }
   JoinInfo* info = static_cast<JoinInfo*>(a.workspace);
   float* pieces = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
-                                           join_bytes(KIND == kShared ? items : kMaxGrid));
+                                           join_bytes(KIND == kShared ? items : kMaxGrid) +
+                                           (a.counted ? counted_shift(M) : 0));
   const bool joins = KIND == kShared || grid > 1;
   launch_kernel(kernel, dim3(grid), dim3(threads), stream, ev.start, joins ? nullptr : ev.stop, a, min_units, info,
                 pieces);

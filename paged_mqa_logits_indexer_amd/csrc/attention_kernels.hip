@@ -80,8 +80,7 @@ size_t attention_workspace_size(int32_t rows, int32_t heads, int32_t requests) {
   if (rows <= 0 || heads <= 0 || requests <= 0) return 0;
   const int64_t together = (static_cast<int64_t>(rows) + requests - 1) / requests * heads;
   const int m = together <= 16 ? 16 : together <= 32 ? 32 : together <= 64 ? 64 : 128;
-  return join_bytes(kMaxGrid) + 2 * kMaxGrid * static_cast<size_t>(piece_floats(m)) * sizeof(float) +
-         kRowCountBytes;
+  return join_bytes(kMaxGrid) + 2 * kMaxGrid * static_cast<size_t>(piece_floats(m)) * sizeof(float);
 }
 
 size_t shared_prefix_workspace_size(int32_t rows, int32_t heads, int32_t requests) {

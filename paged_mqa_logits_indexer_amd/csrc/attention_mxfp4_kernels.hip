@@ -385,7 +385,7 @@ constexpr double kFixed[2][4] = {{19, 22, 27, 47}, {17, 18, 24, 45}};
 // Tiles of a row's list up to the last one that holds a key (at least one): a wave per
 // row, from the end.
 __global__ __launch_bounds__(256) void count_tiles_kernel(const int32_t* __restrict__ indices, int rows, int k,
-                                                          int capacity, int32_t* __restrict__ tiles) {
+                                                          int capacity, uint8_t* __restrict__ tiles) {
   const int row = blockIdx.x * 4 + static_cast<int>(threadIdx.x) / kWave, lane = lane_id();
   if (row >= rows) return;
   const int32_t* list = indices + static_cast<int64_t>(row) * k;
@@ -404,7 +404,7 @@ __global__ __launch_bounds__(256) void count_tiles_kernel(const int32_t* __restr
       if (live && last == 0) last = end - i * kWave - static_cast<int>(__builtin_clzll(live));
     }
   }
-  if (lane == 0) tiles[row] = max(1, (last + kTile - 1) / kTile);
+  if (lane == 0) tiles[row] = static_cast<uint8_t>(max(1, (last + kTile - 1) / kTile));
 }
 
 // Selections of rows that see fewer keys than the list has places end in padding: with
@@ -418,13 +418,11 @@ hipError_t launch(AttentionArgs a, hipStream_t stream, LaunchEvents ev) {
   if constexpr (KIND == kSparse) {
     const int64_t tiles = (a.k + kTile - 1) / kTile, items = item_count<KIND, M>(a);
     if (tiles > 1 && items * tiles >= kCountFrom && (a.cu_q || items > kMaxGrid / 2)) {
-      int32_t* counts = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) +
-                                                   attention_workspace_size(a.rows, a.heads, a.requests) - kRowCountBytes);
       launch_kernel(count_tiles_kernel, dim3((a.rows + 3) / 4), dim3(256), stream, ev.start, nullptr, a.indices, a.rows,
-                    a.k, a.max_pages * kPage, counts);
+                    a.k, a.max_pages * kPage, row_tiles(a));
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      a.row_lens = counts;
+      a.counted = 1;
       ev.start = nullptr;
     }
   }

@@ -299,7 +299,7 @@ struct AttentionArgs {
   const void* cache;
   const int32_t* block_table;    // [requests][max_pages]
   const int32_t* cu_q;           // [requests + 1], or null: next_n rows per request
-  const int32_t* row_lens;       // [rows] end of the keys (dense); sparse: tiles of the list that hold a key, or null
+  const int32_t* row_lens;       // [rows] end of the keys (dense)
   const int32_t* row_starts;     // [rows] first key, or null: 0 (dense)
   const int32_t* row_positions;  // [rows] position the bias counts from, or null: row_lens - 1
   const int32_t* indices;        // [rows][k] selected keys (sparse)
@@ -318,6 +318,7 @@ struct AttentionArgs {
   int32_t max_pages;
   int32_t k;
   int32_t prefix_pages;
+  int32_t counted;               // the workspace holds the tiles of each row's list that hold a key (sparse)
 };
 
 }  // namespace pmqa
