@@ -376,14 +376,35 @@ __device__ __forceinline__ Item make_item(const AttentionArgs& a, int id) {
   }
 }
 
+template <int KIND>
+__host__ __device__ __forceinline__ int64_t item_count(const AttentionArgs& a, int m) {
+  const int64_t pairs = static_cast<int64_t>(a.rows) * a.heads;
+  if (KIND == kSparse) return static_cast<int64_t>(a.rows) * ((a.heads + m - 1) / m);
+  const int64_t own = a.cu_q ? pairs / m + a.requests
+                             : static_cast<int64_t>(a.requests) * ((static_cast<int64_t>(a.next_n) * a.heads + m - 1) / m);
+  return KIND == kShared ? (pairs + m - 1) / m + own : own;
+}
 template <int KIND, int M>
 __host__ __device__ __forceinline__ int64_t item_count(const AttentionArgs& a) {
-  const int64_t pairs = static_cast<int64_t>(a.rows) * a.heads;
-  if (KIND == kSparse) return static_cast<int64_t>(a.rows) * ((a.heads + M - 1) / M);
-  const int64_t own = a.cu_q ? pairs / M + a.requests
-                             : static_cast<int64_t>(a.requests) * ((static_cast<int64_t>(a.next_n) * a.heads + M - 1) / M);
-  return KIND == kShared ? (pairs + M - 1) / M + own : own;
+  return item_count<KIND>(a, M);
 }
+
+// find_share adds up the list a chunk at a time, as many items as the workgroup has
+// threads, and keeps the sums in LDS: a kernel takes lists of up to kChunks chunks.
+// Pair tiles of a size whose list is longer are not chosen (tile_pairs).  The widest
+// tiles that a call may take always fit: at most 65535 items over selections, a
+// request's 4096 more over pages, and twice that with a shared prefix.
+template <int KIND>
+struct ScanOf256 {  // threads
+  static constexpr int kThreads = 256, kChunks = KIND == kSparse ? 644 : 1056;
+  static constexpr int64_t kItems = int64_t{kThreads} * kChunks;
+  static_assert(kItems >= (KIND == kShared ? 2 : 1) * (IDX_MAX_ROWS + IDX_MAX_REQUESTS), "the widest tiles fit");
+};
+template <int KIND>
+struct ScanOf512 {
+  static constexpr int kThreads = 512, kChunks = KIND == kShared ? 2080 : 1056;
+  static constexpr int64_t kItems = int64_t{kThreads} * kChunks;
+};
 
 // The workgroup's share [t0, t1) of the tile list and the item it starts in.
 struct Share {
@@ -656,9 +677,10 @@ int64_t pairs_together(const AttentionArgs& a) {
 
 // Size of the pair tiles: the one whose estimated time is least, from what a
 // workgroup spends on each 64-key tile and on the call (16 / 32 / 64 / 128 pairs).
-// Tiles wider than the pairs would only idle.
+// Tiles wider than the pairs would only idle.  narrowest: the longest list of the
+// kernel for 16 pairs.
 template <int KIND>
-int tile_pairs(const AttentionArgs& a, const double (&per_tile)[4], const double (&fixed)[4]) {
+int tile_pairs(const AttentionArgs& a, const double (&per_tile)[4], const double (&fixed)[4], int64_t narrowest) {
   constexpr int kSizes[] = {16, 32, 64, 128};
   const int64_t together = pairs_together<KIND>(a);
   int best = 16;
@@ -666,6 +688,7 @@ int tile_pairs(const AttentionArgs& a, const double (&per_tile)[4], const double
   for (int i = 0; i < 4; ++i) {
     const int m = kSizes[i];
     if (i > 0 && together <= m / 2) break;
+    if (item_count<KIND>(a, m) > (i == 0 ? narrowest : ScanOf256<KIND>::kItems)) continue;
     const int64_t pairs = static_cast<int64_t>(a.rows) * a.heads;
     double tiles;
     if (KIND == kSparse) {

@@ -58,7 +58,7 @@ hipError_t launch(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
 
 template <int DT, int KIND>
 hipError_t launch_kind(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
-  switch (tile_pairs<KIND>(a, kPerTile, kFixed)) {
+  switch (tile_pairs<KIND>(a, kPerTile, kFixed, ScanOf256<KIND>::kItems)) {
     case 16: return launch<DT, KIND, 16>(a, stream, ev);
     case 32: return launch<DT, KIND, 32>(a, stream, ev);
     case 64: return launch<DT, KIND, 64>(a, stream, ev);

@@ -59,13 +59,12 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
   using E = Elem<DT>;
   constexpr int M = 16;
   constexpr int kBlocksPerTile = kTile / kOwnKeys;
-  // (work lists: at most 2^16 rows of 8 pair tiles and a request's more, twice that with a shared prefix)
-  constexpr int kScan = kWaves + (KIND == kShared ? 2080 : 1056);
+  static_assert(ScanOf512<KIND>::kThreads == kThreads, "chunks of the work list");
   __shared__ __attribute__((aligned(1024))) char s_ring[kOwnRing];
   __shared__ float2 s_ml[kWaves][16];
   __shared__ PairInfo s_pair[M];
   __shared__ int64_t s_res[2];
-  __shared__ int s_scan[kScan];
+  __shared__ int s_scan[kWaves + ScanOf512<KIND>::kChunks];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grid = gridDim.x;
@@ -432,7 +431,7 @@ hipError_t launch(AttentionArgs a, hipStream_t stream, LaunchEvents ev) {
 
 template <int DT, int KIND>
 hipError_t launch_kind(const AttentionArgs& a, hipStream_t stream, LaunchEvents ev) {
-  switch (tile_pairs<KIND>(a, kPerTile[KIND == kSparse], kFixed[KIND == kSparse])) {
+  switch (tile_pairs<KIND>(a, kPerTile[KIND == kSparse], kFixed[KIND == kSparse], ScanOf512<KIND>::kItems)) {
     case 16: return launch<DT, KIND, 16>(a, stream, ev);
     case 32: return launch<DT, KIND, 32>(a, stream, ev);
     case 64: return launch<DT, KIND, 64>(a, stream, ev);

@@ -14,7 +14,6 @@ constexpr int kBlkBytes = 2 * kOctBytes;           // 16 keys
 constexpr int kRingBytes = 2 * kTile * kRowBytes;  // 147456: 128 keys in all slots together
 constexpr int kWindow = 2048;                      // sparse: keys whose cache rows are resolved at a time
 constexpr int kAttnThreads = 256;
-constexpr int kScanChunks = 1056;                  // work-list chunks of 256 pair tiles
 
 // LDS image of 8 keys (9 KiB): nine 1 KiB pieces, each holding 128 bytes of
 // every key -- what one direct-to-LDS load of 64 x 16 bytes writes.  Within
@@ -189,7 +188,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attention_kernel(AttentionArg
   __shared__ float2 s_ml[4][S::kWavePairs];
   __shared__ PairInfo s_pair[S::kWavePairs * S::kGroups];
   __shared__ int64_t s_res[2];
-  __shared__ int s_scan[KIND == kSparse ? 8 + 640 : kAttnThreads / kWave + kScanChunks];
+  static_assert(ScanOf256<KIND>::kThreads == kAttnThreads, "chunks of the work list");
+  __shared__ int s_scan[kAttnThreads / kWave + ScanOf256<KIND>::kChunks];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grid = gridDim.x;

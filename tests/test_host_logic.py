@@ -29,3 +29,11 @@ def test_bin_key_ranges_match_the_bins_of_every_half(tmp_path):
     res = _build_and_run("bin_ranges_check.hip", tmp_path)
     assert res.returncode == 0, res.stdout + res.stderr
     assert "mismatches 0" in res.stdout
+
+
+def test_work_lists_fit_their_counters(tmp_path):
+    # Which size the attention's pair tiles have goes by estimated times; no
+    # table of times may choose one whose list overruns the kernel's counters.
+    res = _build_and_run("work_list_check.hip", tmp_path)
+    assert res.returncode == 0, res.stdout + res.stderr
+    assert "mismatches 0" in res.stdout
