@@ -433,6 +433,7 @@ idx_status axis_rotations(const int32_t* positions, int32_t axes, uint64_t axis_
   a.axes = axes;
   a.axis_map = axis_map;
   a.tokens = tokens;
+  a.position_stride = tokens;
   a.rope = rope;
   a.max_positions = max_positions;
   a.out = out;
@@ -447,7 +448,7 @@ idx_status rotate_queries(const void* x, int64_t x_token_stride, int64_t x_head_
                           int64_t out_token_stride, int64_t out_head_stride, void* stream) {
   const pmqa::LaunchEvents ev = take_events();
   pmqa::RotaryArgs a{x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, positions, rope,
-                     axis_map, axes, dtype, max_positions, interleaved, tokens, heads};
+                     axis_map, axes, dtype, max_positions, interleaved, tokens, heads, tokens};
   idx_status st = check_rotary(a);
   if (!x || heads <= 0) return IDX_EINVAL;
   if (st != IDX_OK) return st;
@@ -474,7 +475,8 @@ idx_status rotate_index_queries(const void* q, int64_t q_token_stride, int64_t q
                                 void* stream) {
   const pmqa::LaunchEvents ev = take_events();
   pmqa::RotaryArgs a{q, q_token_stride, q_head_stride, codes, IDX_NUM_HEADS * IDX_HEAD_DIM, IDX_HEAD_DIM, positions,
-                     rope, axis_map, axes, dtype, max_positions, interleaved, tokens, IDX_NUM_HEADS};
+                     rope, axis_map, axes, dtype, max_positions, interleaved, tokens, IDX_NUM_HEADS,
+                     tokens};
   idx_status st = check_rotary(a);
   if (!q) return IDX_EINVAL;
   if (st != IDX_OK) return st;

@@ -248,7 +248,7 @@ struct RotaryArgs {
   void* out;
   int64_t out_token_stride;
   int64_t out_head_stride;
-  const int32_t* positions;  // [axes][tokens]
+  const int32_t* positions;  // [axes][tokens], axes position_stride apart
   const float* rope;         // [max_positions][64]
   uint64_t axis_map;         // two bits per angle: its axis
   int32_t axes;
@@ -257,6 +257,7 @@ struct RotaryArgs {
   int32_t interleaved;
   int32_t tokens;
   int32_t heads;
+  int64_t position_stride;   // all of a call's tokens
 };
 
 // Release, fork and compaction of the pages of a pool.

@@ -11,21 +11,15 @@ namespace {
 constexpr int kRope = IDX_ROPE_DIM;        // 64 rotated dimensions
 constexpr int kHalfRope = kRope / 2;       // 32 angles
 
-// Grid of the rotation of [tokens][heads] rows: workgroups of 32 heads of a token side
-// by side on x, kSlabTokens tokens of them to a step of z.  (An extent of a grid is
-// counted in threads, below 2^32: with all of 2^24 tokens on x, one head each, it is
-// 2^32; a slab of 128 heads is 2^31.)
+// The rotation of [tokens][heads] rows: workgroups of 32 heads of a token, and launches
+// of up to kSlabTokens tokens.  (A grid is counted in threads, below 2^32: 2^24 tokens
+// of one head in one launch have 2^32, a slab of 128 heads has 2^31.)
 constexpr int kRotateThreads = 256;
 constexpr int kHeadsPerWg = kRotateThreads / 8;
 constexpr int kSlabTokens = 1 << 21;
-struct RotateGrid {
-  int chunks;     // workgroups of a token
-  uint32_t x, z;
-};
-inline RotateGrid rotate_grid(int32_t tokens, int32_t heads) {
-  const int chunks = (heads + kHeadsPerWg - 1) / kHeadsPerWg;
-  const int side = tokens < kSlabTokens ? tokens : kSlabTokens;
-  return {chunks, static_cast<uint32_t>(side) * chunks, static_cast<uint32_t>((tokens + kSlabTokens - 1) / kSlabTokens)};
+inline int chunks_of(int32_t heads) { return (heads + kHeadsPerWg - 1) / kHeadsPerWg; }
+inline uint32_t rotate_workgroups(int32_t tokens, int32_t heads) {
+  return static_cast<uint32_t>(tokens) * chunks_of(heads);
 }
 
 struct F32Row {

@@ -33,7 +33,7 @@ __device__ __forceinline__ AxisPositions axis_positions(const RotaryArgs& a, int
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int axis = min(i, a.axes - 1);
-    p.at[i] = max(0, min(a.positions[static_cast<int64_t>(axis) * a.tokens + token], a.max_positions - 1));
+    p.at[i] = max(0, min(a.positions[axis * a.position_stride + token], a.max_positions - 1));
   }
   return p;
 }
@@ -78,8 +78,7 @@ template <int DT, bool INDEX>
 __global__ __launch_bounds__(kRotateThreads) void rotate_kernel(RotaryArgs a, int chunks) {
   constexpr int kBytes = DT == IDX_FP32 ? 4 : 2, kPiece = 8 * kBytes, kPieces = kRope / 8;
   __shared__ __attribute__((aligned(16))) float s_row[kRope];
-  const int token = blockIdx.z * kSlabTokens + blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  if (token >= a.tokens) return;  // (whole workgroups of the last slab)
+  const int token = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int piece = threadIdx.x % kPieces, head = chunk * kHeadsPerWg + static_cast<int>(threadIdx.x) / kPieces;
   const bool here = head < a.heads;
   const char* row = static_cast<const char*>(a.x) +
@@ -111,11 +110,23 @@ __global__ __launch_bounds__(kRotateThreads) void rotate_kernel(RotaryArgs a, in
   }
 }
 
+// One launch, or one for each slab of tokens.
 template <int DT, bool INDEX>
-void launch_rotate(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev) {
-  const RotateGrid grid = rotate_grid(a.tokens, a.heads);
-  launch_kernel(rotate_kernel<DT, INDEX>, dim3(grid.x, 1, grid.z), dim3(kRotateThreads), stream, ev.start, ev.stop, a,
-                grid.chunks);
+hipError_t launch_rotate(RotaryArgs a, hipStream_t stream, LaunchEvents ev) {
+  constexpr int kBytes = DT == IDX_FP32 ? 4 : 2;
+  const int32_t all = a.tokens;
+  for (int32_t first = 0; first < all; first += a.tokens) {
+    a.tokens = all - first < kSlabTokens ? all - first : kSlabTokens;
+    const bool last = first + a.tokens == all;
+    launch_kernel(rotate_kernel<DT, INDEX>, dim3(rotate_workgroups(a.tokens, a.heads)), dim3(kRotateThreads), stream,
+                  first == 0 ? ev.start : nullptr, last ? ev.stop : nullptr, a, chunks_of(a.heads));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || last) return e;
+    a.positions += a.tokens;
+    a.x = static_cast<const char*>(a.x) + a.tokens * a.x_token_stride * kBytes;
+    a.out = static_cast<char*>(a.out) + a.tokens * a.out_token_stride * (INDEX ? 1 : kBytes);
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -128,16 +139,14 @@ hipError_t launch_axis_rotations(const RotaryArgs& a, hipStream_t stream, Launch
 }
 
 hipError_t launch_rotate_queries(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev) {
-  if (a.dtype == IDX_BF16) launch_rotate<IDX_BF16, false>(a, stream, ev);
-  else launch_rotate<IDX_FP16, false>(a, stream, ev);
-  return hipGetLastError();
+  return a.dtype == IDX_BF16 ? launch_rotate<IDX_BF16, false>(a, stream, ev)
+                             : launch_rotate<IDX_FP16, false>(a, stream, ev);
 }
 
 hipError_t launch_rotate_index_queries(const RotaryArgs& a, hipStream_t stream, LaunchEvents ev) {
-  if (a.dtype == IDX_BF16) launch_rotate<IDX_BF16, true>(a, stream, ev);
-  else if (a.dtype == IDX_FP16) launch_rotate<IDX_FP16, true>(a, stream, ev);
-  else launch_rotate<IDX_FP32, true>(a, stream, ev);
-  return hipGetLastError();
+  if (a.dtype == IDX_BF16) return launch_rotate<IDX_BF16, true>(a, stream, ev);
+  if (a.dtype == IDX_FP16) return launch_rotate<IDX_FP16, true>(a, stream, ev);
+  return launch_rotate<IDX_FP32, true>(a, stream, ev);
 }
 
 }  // namespace pmqa

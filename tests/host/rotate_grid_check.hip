@@ -1,6 +1,6 @@
-// Host-side check of the rotation's grid over every number of heads and token counts
-// from 1 to the most: an extent in threads stays below 2^32, every token has its
-// workgroups in one slab, and no slab is empty.
+// Host-side check of the rotation's launches over every number of heads and token
+// counts from 1 to the most of a launch: workgroups for every head of every token, and
+// an extent of the grid below 2^32 threads.
 #include <cstdio>
 
 #include "rotary.h"
@@ -9,17 +9,17 @@ int main() {
   using namespace pmqa;
   long bad = 0, checked = 0;
   for (int heads = 1; heads <= IDX_MAX_ATTENTION_HEADS; ++heads) {
-    for (int32_t power = 1; power <= IDX_MAX_APPEND_TOKENS; power *= 2) {
+    for (int64_t power = 1; power <= IDX_MAX_APPEND_TOKENS; power *= 2) {
       for (int d = -3; d <= 3; ++d) {
-        const int32_t tokens = power + d;
-        if (tokens < 1 || tokens > IDX_MAX_APPEND_TOKENS) continue;
-        const RotateGrid g = rotate_grid(tokens, heads);
-        const uint64_t threads = static_cast<uint64_t>(g.x) * kRotateThreads;
-        const uint64_t side = g.x / g.chunks;  // tokens of a slab
-        const bool ok = threads < (uint64_t{1} << 32) && g.z >= 1 && g.z <= 65535 && g.x % g.chunks == 0 &&
-                        g.chunks * kHeadsPerWg >= heads && (g.z == 1 || side == kSlabTokens) &&
-                        g.z * side >= static_cast<uint64_t>(tokens) && (g.z - 1) * side < static_cast<uint64_t>(tokens);
-        if (!ok && bad++ < 10) std::printf("%d tokens of %d heads: grid %u x %u\n", tokens, heads, g.x, g.z);
+        const int64_t all = power + d;
+        if (all < 1 || all > IDX_MAX_APPEND_TOKENS) continue;
+        const int32_t tokens = static_cast<int32_t>(all < kSlabTokens ? all : kSlabTokens);
+        const uint64_t workgroups = rotate_workgroups(tokens, heads);
+        const bool ok = workgroups * kRotateThreads < (uint64_t{1} << 32) &&
+                        workgroups * kHeadsPerWg >= static_cast<uint64_t>(tokens) * heads &&
+                        workgroups == static_cast<uint64_t>(tokens) * chunks_of(heads);
+        if (!ok && bad++ < 10)
+          std::printf("%d tokens of %d heads: %llu workgroups\n", tokens, heads, static_cast<unsigned long long>(workgroups));
         ++checked;
       }
     }

@@ -46,6 +46,23 @@ def test_most_query_rows(gpu, tokens, heads):
 
 
 @pytest.mark.gpu
+def test_slabs_on_several_axes(gpu):
+    """Tokens of a second launch: their positions on every axis, their rows, in and out."""
+    tokens, heads, axis_of = (1 << 21) + 5, 2, [0] * 8 + [1] * 12 + [2] * 12
+    announce(f"rotate_queries {tokens} x {heads} on three axes")
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(tokens, heads, 64, dtype=torch.bfloat16, device=DEV)
+    rope, amap = table(), gpu.axis_map(axis_of)
+    at = torch.randint(0, POSITIONS, (3, tokens), generator=g).int().to(DEV)
+    out = torch.empty(tokens, heads, 64, dtype=torch.bfloat16, device=DEV)
+    gpu.rotate_queries(x, at, rope, out, amap)
+    want = torch.empty(40, heads, 64, dtype=torch.bfloat16, device=DEV)
+    gpu.rotate_queries(x[-40:], at[:, -40:].contiguous(), rope, want, amap)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-40:], want)
+
+
+@pytest.mark.gpu
 def test_most_index_rows(gpu):
     tokens = (1 << 21) + 3
     announce(f"rotate_index_queries {tokens}")
