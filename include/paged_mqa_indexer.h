@@ -568,7 +568,11 @@ idx_status rotate_queries(const void* x, int64_t x_token_stride, int64_t x_head_
 /*
  * rotate_index_queries -- the indexer's queries as indexer_logits reads them: the
  * first 64 of 128 dimensions rotated (rounded once to float32), all of them clamped
- * to +-448 and rounded to E4M3 codes, nearest even; NaN stays NaN.
+ * to +-448, infinities among them, and rounded to E4M3 codes, nearest even; NaN stays
+ * NaN.  Values are not scaled: a caller whose queries pass 448, or lie mostly below
+ * E4M3's normal values (2^-6), divides a head's row by a factor of its own first and
+ * multiplies the row's weight of that head by it (the logits are sums of weight times
+ * max(0, product), so the factor, above 0, passes through).
  *
  * q            (device) [tokens][32] rows of 128, dtype BF16, FP16 or FP32, strides
  *              as above

@@ -812,7 +812,8 @@ def rotate_index_queries(q, positions, rope, codes, axis_map=0, interleaved=Fals
 
     q [tokens, 32, 128] bfloat16, float16 or float32 with 16-byte rows; codes
     [tokens, 32, 128] uint8; other arguments as for rotate_queries.  Values beyond
-    +-448 become +-448.
+    +-448, infinities among them, become +-448; nothing is scaled: divide a head's
+    row by a factor beforehand and multiply its weight by it where that matters.
     """
     dev, dtype = q.device, q.dtype
     if dtype not in VALUE_DTYPES:

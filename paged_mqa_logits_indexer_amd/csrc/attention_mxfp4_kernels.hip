@@ -15,14 +15,16 @@
 // product takes them in -- a lane's 16 bytes are one block of 32 dimensions, one
 // power of two -- and go from there through LDS, where the second product reads them
 // transposed.  No wave waits for another before the output.  (The 32-pair form of the
-// other kernel, on 16 heads: 1 request of 2048 keys 22 instead of 19 us, 16 of 32768
-// keys 97 instead of 56.)
+// other kernel, on 16 heads: 1 request of 2048 keys 21 instead of 18 us, 16 of 32768
+// keys 88 instead of 49.)
 //
 // Measured (MI355X; kernels, medians under the kernel trace): 64 requests of 1 .. 32768
-// keys with 16 heads 33.5 us (85 MB of keys; over 16 bits 54); calls: 64 requests of 32768
-// keys 200 us (839 MB, 4.2 TB/s; over 16 bits 402), 16 requests of 32768 keys with 128
-// heads 195 us (749 TFLOP/s; over 16 bits 195), 512 rows of 128 heads over 2048 listed
-// keys 358 us (816 TFLOP/s; 358), one request of 65 keys 10.5 us.  With few heads the K
+// keys with 16 heads, capped and biased, 34 us (85 MB of keys; over 16 bits 54), one
+// request of 65 keys 10.5.  Calls of the C entry points, in turn with those over 16 bits
+// (in brackets): 64 requests of 32768 keys 168 us (839 MB, 5.0 TB/s, partly from the
+// last-level cache; 401), 16 requests of 32768 keys with 128 heads 185 us (790 TFLOP/s;
+// 186), 512 rows of 128 heads over 2048 listed keys 317 us (922 TFLOP/s; 306), a third
+// of the places empty 238 (287), one request of 65 keys 10.8 (9.6).  With few heads the K
 // stream bounds it, with many the MFMAs and what stands between them, as over 16 bits;
 // unpacking is 0 to 5 % of the wide form's time.
 #include "attention_tiles.h"
@@ -43,9 +45,13 @@ __device__ __forceinline__ s16x8 finite_or_zero(s16x8 x) {
   return x;
 }
 
-// What taking up and writing a pair tile counts for in tiles, whose time here is short
-// (calls with 3, as in the other kernel, 6, 9 and 12: 64 requests of 1 .. 32768 keys 43 /
-// 36 / 36 / 36 us, of 64 keys 22 / 16 / 17 / 17, 256 of 1 .. 4096 keys 39 / 38 / 40 / 41).
+// What taking up and writing a pair tile counts for in tiles, whose time here is short.
+// Calls of 16 heads with 3, as in the other kernel, 6, 8, 9 and 12: 64 requests of 1 ..
+// 32768 keys 41.1 / 34.1 / 33.7 / 33.7 / 34.1 us, of 64 keys 18.7 / 13.2 / 13.4 / 12.7 /
+// 13.7, of 512 keys 25.4 / 23.0 / 22.8 / 23.1 / 24.2, 256 of 1 .. 4096 keys 38.4 / 36.4 /
+// 36.2 / 37.7 / 38.8, 4 of 8192 keys 20.3 / 20.0 / 20.3 / 20.2 / 20.2; selections that are
+// counted (600 rows, 900 of 2048 places) 84.3 / 83.3 / 82.9 / 83.3 / 83.6, and ragged
+// (200 rows, 2048 places) 62.1 / 61.2 / 62.2 / 62.2 / 62.2.
 constexpr int kOwnCost = 8;
 constexpr int kOwnKeys = 16;                 // keys that a wave takes at a time
 constexpr int kOwnOctet = 8 * 1024;              // LDS image of 8 keys: their values alone
@@ -373,11 +379,12 @@ __global__ __launch_bounds__(kThreads, 2) void own_keys_kernel(AttentionArgs a, 
 // Microseconds of a workgroup per 64-key tile, and of a call, over pages and over
 // selections (whose keys each pair tile gathers for itself), from every size forced on
 // selections of 512 and 2048 keys for 1 .. 256 rows of 32, 64 and 128 heads, and on 1
-// .. 64 requests of 512 .. 32768 keys with 16 .. 128 heads.  Between them (16 / 32 / 64
-// / 128 pairs): 64 rows of 32 heads over 2048 keys 47 / 45 / 54 / 73 us, 256 rows of 64
-// heads 190 / 173 / 129 / 190, of 128 heads 369 / 336 / 250 / 213; 16 requests of 32768
-// keys with 32 heads 86 / 98 / 128 / 173, with 64 heads 148 / 161 / 132 / 179, with 128
-// heads 267 / 297 / 225 / 200.
+// .. 64 requests of 512 .. 32768 keys with 16 .. 128 heads (the entries for 16 pairs with
+// an item's cost of 3, before it was 8).  Between them (16 / 32 / 64 / 128 pairs, the
+// cost 8): 64 rows of 32 heads over 2048 keys 43 / 42 / 50 / 63 us, 256 rows of 64 heads
+// 177 / 160 / 119 / 161, of 128 heads 338 / 310 / 230 / 169; 16 requests of 32768 keys
+// with 32 heads 79 / 90 / 120 / 160, with 64 heads 143 / 154 / 124 / 171, with 128 heads
+// 262 / 291 / 221 / 190.
 constexpr double kPerTile[2][4] = {{0.95, 2.1, 3.1, 4.8}, {1.35, 2.4, 3.45, 5.0}};
 constexpr double kFixed[2][4] = {{19, 22, 27, 47}, {17, 18, 24, 45}};
 
@@ -409,7 +416,8 @@ __global__ __launch_bounds__(256) void count_tiles_kernel(const int32_t* __restr
 // Selections of rows that see fewer keys than the list has places end in padding: with
 // enough tiles for a workgroup, those behind a row's last key are counted out before
 // the list is shared.  (512 rows of 128 heads, 2048 places, a third of the tiles empty:
-// 262 us, with all of them 349; none empty: 358 and 353.)
+// 239 us, with all of them 327; none empty: 317 and 312.  1024 rows of 16 heads: 139 and
+// 177; 300 of 704 places, 200 keys: 35 and 43, none empty: 47 and 43.)
 constexpr int kCountFrom = 4 * kMaxGrid;
 
 template <int DT, int KIND, int M>

@@ -14,9 +14,10 @@
 //            page below L (both ascending), so sources and destinations never meet
 //   copy     (source, destination) pages in every cache, whole or their first tokens
 //
-// Copies are bound by memory (229 pages in 24 caches, 62 MB to and fro, 11.5 us: 5.4
-// TB/s, partly from the last-level cache), the rest by its few dependent round trips
-// (a pool of 1000 pages: release 2.4, fork 5.6, compact 6.1 us).
+// Copies are bound by memory (about 114 pages in 24 caches, 62 MB read and written
+// together, 11.2 us: 5.5 TB/s, partly from the last-level cache), the rest by its few
+// dependent round trips (release 2.4, fork 5.5 us for 64 requests, compact 6.1 us for a
+// pool of 478 pages).
 //
 // The results are whole numbers and do not depend on timing: refs change by atomic
 // additions alone, and every list is ordered by a scan.

@@ -13,8 +13,9 @@
 //   rotate_index_queries  the first 64 of 128 dimensions; all of them to E4M3 codes,
 //                         clamped to +-448, which indexer_logits reads
 //
-// Each value is rounded once (rotary.h).  Bound by memory: 4096 rows of 128 heads, of
-// 384 and 1152 bytes apart, move 134 MB in 34 us (3.9 TB/s; three axes 38 us).
+// Each value is rounded once (rotary.h).  Bound by memory: 4096 rows of 128 heads on
+// three axes, 384 and 1152 bytes apart, move 134 MB in 29 us under the kernel trace (4.6
+// TB/s; calls 30.5 us, on one axis 29.8).
 #include "indexer_common.h"
 #include "launches.h"
 #include "rotary.h"
@@ -69,11 +70,12 @@ __device__ __forceinline__ int2 clamped_codes(F32Row x) {
 
 // A workgroup per 32 heads of a token, 8 threads per head, each with 8 rotated
 // dimensions and, of an index query, 8 of the others (with 16 threads, of which half
-// rotate in float64, 4001 rows of 32 heads 17.8 us instead of 13.7).  The angles are
-// read from the table, or, on several axes, gathered in LDS by 64 threads (each thread
-// its own: 4096 rows of 128 heads 58 us instead of 38).  The queries are asked for
-// first, beside the chain position, table row, angles.  What is written goes past the
-// caches (38 instead of 40 us); several heads per thread measured 40 and 41 us.
+// rotate in float64, 4001 rows of 32 heads took 1.3 times as long when it was tried).
+// The angles are read from the table, or, on several axes, gathered in LDS by 64
+// threads (each thread its own: half as long again, 4096 rows of 128 heads, likewise).
+// The queries are asked for first, beside the chain position, table row, angles.  What
+// is written goes past the caches, which it would only fill (30.5 us a call with it,
+// 30.3 without: the rows of one call alone do not show it).
 template <int DT, bool INDEX>
 __global__ __launch_bounds__(kRotateThreads) void rotate_kernel(RotaryArgs a, int chunks) {
   constexpr int kBytes = DT == IDX_FP32 ? 4 : 2, kPiece = 8 * kBytes, kPieces = kRope / 8;
